@@ -82,8 +82,25 @@ typedef enum {
   SIG_OP_SPARSE_GEMV_BATCH = 6, /* sparse_gemv_batch(d_in, d_out, rows = tokens) */
   SIG_OP_SPARSE_GEMV_Q8 = 7,    /* sparse_gemv_q8(d_in, d_out)              */
   SIG_OP_SPARSE_GEMV_F8 = 8,    /* sparse_gemv_f8(d_in, d_out)              */
-  SIG_OP_SPARSE_GEMV_Q4 = 9     /* sparse_gemv_q4(d_in, d_out)              */
+  SIG_OP_SPARSE_GEMV_Q4 = 9,    /* sparse_gemv_q4(d_in, d_out)              */
+  SIG_OP_GATED_TOKENS = 10,     /* gated_mlp(d_model = d_in, d_ff = d_out, rows) */
+  SIG_OP_GATED_BACKWARD = 11    /* gated_mlp_backward(d_model = d_in, d_ff = d_out, rows) */
 } sig_op;
+
+/* Types of the 16-bit values of linear_act, gated_mlp and gated_mlp_backward. */
+typedef enum {
+  SIG_F16 = 0,   /* IEEE binary16                                      */
+  SIG_BF16 = 1   /* bfloat16: the upper half of an IEEE binary32       */
+} sig_dtype;
+
+/* Activations of linear_act, gated_mlp and gated_mlp_backward, in float32. */
+typedef enum {
+  SIG_ACT_NONE = 0,       /* z                                               */
+  SIG_ACT_RELU = 1,       /* max(z, 0); slope 0 at z = 0, NaN stays NaN      */
+  SIG_ACT_GELU = 2,       /* z Phi(z), Phi the normal distribution function  */
+  SIG_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2 */
+  SIG_ACT_SILU = 4        /* z / (1 + exp(-z))                               */
+} sig_act;
 
 /* Largest activation length the fused mask prologue accepts. */
 #define SIG_MAX_D_IN 131072
@@ -517,6 +534,91 @@ SIG_API int gated_mlp_sparse_noalloc(const uint16_t* x, const uint16_t* WgT, con
                                      sig_stream_t stream);
 
 /*
+ * Dense linear layer for a block of tokens, with bias, activation and residual
+ * in the product's epilogue (the pages have no counterpart: it is the layer of
+ * sparse_gemv for a prompt, a training block or a batch of decoded tokens,
+ * whose masks differ too much to skip weight rows):
+ *   Y = act(X WT + bias) + residual
+ * float32 accumulation on the tensor cores, the epilogue in float32, Y rounded
+ * once.  A row of Y depends on that row of X and of the residual only.
+ *   dtype    SIG_F16 or SIG_BF16, the type of every buffer.
+ *   X        [rows x K], row r at X + r ldx.
+ *   WT       [K x N], contiguous.
+ *   bias     [N], nullable.
+ *   act      a sig_act.
+ *   residual [rows x N], row r at residual + r ldr; nullable (ldr is ignored then).
+ *   Y        [rows x N] out, row r at Y + r ldy; entries between rows are left
+ *            as they were.  Y may be the residual buffer itself (same pointer
+ *            and stride); it must not overlap anything else that is read.
+ * 0 <= rows <= 2^24 (0: nothing is read or written), 1 <= K <= 2^20,
+ * 8 <= N <= 2^20, N % 8 == 0; each stride at least its row's length, a multiple
+ * of 8 and at most 2^30; every pointer 16-byte aligned.
+ * Bit-identical from run to run (sums in a fixed order).
+ * Errors: SIG_ERR_NULL, SIG_ERR_ARG (dtype, act), SIG_ERR_SHAPE, SIG_ERR_ALIGN
+ *         (pointers; a stride that is not a multiple of 8), SIG_ERR_CUDA.
+ */
+SIG_API int linear_act(const uint16_t* X, int64_t rows, int64_t K, int64_t ldx,
+                       const uint16_t* WT, int64_t N, const uint16_t* bias, int act,
+                       const uint16_t* residual, int64_t ldr, uint16_t* Y, int64_t ldy, int dtype,
+                       sig_stream_t stream);
+
+/*
+ * Gated MLP for a block of tokens (the dense form of gated_mlp_sparse and
+ * teal_mlp_sparse, Eqn. 12's gate and up projections with no mask):
+ *   g = X WgT, u = X WuT, h = act(g) . u   (one kernel: both projections, the
+ *                                           activation and the product)
+ *   Y = h WdT + residual                   (as linear_act)
+ * float32 accumulation; h is computed from the float32 g and u and rounded
+ * once to the 16-bit type, the operand type of the down projection.
+ *   X [rows x d_model], row r at X + r ldx.  WgT, WuT [d_model x d_ff].
+ *   WdT [d_ff x d_model].  residual, Y [rows x d_model] with strides, as
+ *   linear_act (residual nullable; Y may be the residual buffer).
+ *   h_out [rows x d_ff] out, contiguous, nullable.
+ *   g_out, u_out [rows x d_ff] out, contiguous, both or neither: what
+ *        gated_mlp_backward needs.
+ *   ws   sig_workspace_bytes(SIG_OP_GATED_TOKENS, d_model, d_ff, rows) bytes,
+ *        256-byte aligned, for h; it needs no initialisation and holds nothing
+ *        from call to call.  NULL when h_out is given.
+ * 0 <= rows <= 2^24, 8 <= d_model, d_ff <= 2^20, both multiples of 8; pointers
+ * and strides as linear_act.  Outputs must not overlap inputs or each other
+ * (but Y the residual).
+ * Errors: as linear_act, SIG_ERR_NULL also for one of g_out and u_out alone,
+ *         SIG_ERR_WORKSPACE.
+ */
+SIG_API int gated_mlp(const uint16_t* X, int64_t rows, int64_t ldx, const uint16_t* WgT,
+                      const uint16_t* WuT, const uint16_t* WdT, int64_t d_model, int64_t d_ff,
+                      int act, const uint16_t* residual, int64_t ldr, uint16_t* Y, int64_t ldy,
+                      uint16_t* h_out, uint16_t* g_out, uint16_t* u_out, int dtype, void* ws,
+                      size_t ws_bytes, sig_stream_t stream);
+
+/*
+ * Gradients of gated_mlp, given the gradient dY of its output and the g and u
+ * that it kept:
+ *   dh = dY WdT^T,  dg = dh . u . act'(g),  du = dh . act(g),  h = act(g) . u
+ *   dX = dg WgT^T + du WuT^T
+ *   dWgT = X^T dg,  dWuT = X^T du,  dWdT = h^T dY
+ * dh stays in float32 inside the kernel that forms dg, du and h; these three
+ * are rounded once to the 16-bit type, the operand type of the products that
+ * follow; every sum is accumulated in float32 and rounded once.  The gradient
+ * of a residual is dY itself.
+ *   dY, X, dX [rows x d_model] with strides.  g, u [rows x d_ff], contiguous.
+ *   WgT, WuT, dWgT, dWuT [d_model x d_ff].  WdT, dWdT [d_ff x d_model].
+ *   dX nullable; dWgT and dWuT both or neither; dWdT nullable; at least one of
+ *   the three.  The gradients are written, not added to.  With rows == 0 the
+ *   weight gradients are set to zero.
+ *   ws   sig_workspace_bytes(SIG_OP_GATED_BACKWARD, d_model, d_ff, rows) bytes,
+ *        256-byte aligned, for dg, du and h; needs no initialisation and holds
+ *        nothing from call to call (NULL for rows == 0).
+ * Limits, alignment and errors as gated_mlp.  Bit-identical from run to run.
+ */
+SIG_API int gated_mlp_backward(const uint16_t* dY, int64_t lddy, const uint16_t* X, int64_t ldx,
+                               int64_t rows, const uint16_t* g, const uint16_t* u,
+                               const uint16_t* WgT, const uint16_t* WuT, const uint16_t* WdT,
+                               int64_t d_model, int64_t d_ff, int act, uint16_t* dX, int64_t lddx,
+                               uint16_t* dWgT, uint16_t* dWuT, uint16_t* dWdT, int dtype, void* ws,
+                               size_t ws_bytes, sig_stream_t stream);
+
+/*
  * Read and clear the library's device error words (no counterpart on the
  * pages; they report the bounded waits: bit 0, a tensor-core GEMM pipeline
  * wait; bit 1, the split-K finish of an fp16 GEMV).  Synchronises `stream`.
@@ -528,8 +630,8 @@ SIG_API int sig_take_device_error(unsigned* code, sig_stream_t stream);
 
 /*
  * Set the limit, in SM clock cycles, after which a pipeline wait of the
- * tensor-core GEMMs (nm_act_gemm, nm_act_gemm_ex, nm_act_gemm_packed) gives
- * up, on the current device; cycles <= 0 restores the default (4e9, about 2 s
+ * tensor-core GEMMs (nm_act_gemm, nm_act_gemm_ex, nm_act_gemm_packed,
+ * linear_act, gated_mlp, gated_mlp_backward) gives up, on the current device; cycles <= 0 restores the default (4e9, about 2 s
  * at 1.9 GHz).  No counterpart on the pages: it lets a caller (or a test)
  * shorten the failure-detection window.  A kernel that gives up records a bit
  * in the device error word (sig_take_device_error), lets the copies it has

@@ -6,7 +6,8 @@ C ABI declared in ``include/sig.h``.  Every step of the computation runs in the
 library's CUDA kernels; there is no other implementation behind these calls.
 Importing this module fails loudly when ``libsig.so`` has not been built.
 
-fp16 tensors are ``torch.float16``; masks are ``torch.int32`` tensors holding
+fp16 tensors are ``torch.float16`` (linear_act, gated_mlp and gated_mlp_backward
+also take ``torch.bfloat16``); masks are ``torch.int32`` tensors holding
 the uint32 bit words (bit i % 32 of word i // 32); index lists are int32.
 """
 from __future__ import annotations
@@ -27,6 +28,8 @@ __all__ = [
     "sparse_gemv_q8", "sparsify_nm_ex", "nm_act_gemm_ex", "col_sums", "teal_mlp_sparse",
     "nm_packed_bytes", "sparsify_nm_packed", "nm_act_gemm_packed", "sparse_gemv_f8",
     "OP_SPARSE_GEMV_F8", "set_wait_limit", "sparse_gemv_q4", "OP_SPARSE_GEMV_Q4",
+    "linear_act", "gated_mlp", "gated_mlp_backward", "ACT_NONE", "ACT_RELU", "ACT_GELU",
+    "ACT_GELU_TANH", "ACT_SILU", "OP_GATED_TOKENS", "OP_GATED_BACKWARD",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsig.so")
@@ -36,6 +39,9 @@ OP_SPARSE_GEMV_BATCH = 6
 OP_SPARSE_GEMV_Q8 = 7
 OP_SPARSE_GEMV_F8 = 8
 OP_SPARSE_GEMV_Q4 = 9
+OP_GATED_TOKENS = 10
+OP_GATED_BACKWARD = 11
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
 MAX_BATCH = 16
 MAX_D_IN = 131072
 
@@ -69,6 +75,11 @@ _SIGNATURES = {
     "sparsify_nm_ex": (_i32, [_p, _i64, _i64, _i32, _i32, _p, _p, _i32, _p, _p, _p, _p]),
     "nm_act_gemm_ex": (_i32, [_p, _i64, _i64, _p, _i64, _i32, _i32, _p, _p, _i32, _p, _p, _p, _sz,
                               _p]),
+    "linear_act": (_i32, [_p, _i64, _i64, _i64, _p, _i64, _p, _i32, _p, _i64, _p, _i64, _i32, _p]),
+    "gated_mlp": (_i32, [_p, _i64, _i64, _p, _p, _p, _i64, _i64, _i32, _p, _i64, _p, _i64, _p, _p,
+                         _p, _i32, _p, _sz, _p]),
+    "gated_mlp_backward": (_i32, [_p, _i64, _p, _i64, _i64, _p, _p, _p, _p, _p, _i64, _i64, _i32,
+                                  _p, _i64, _p, _p, _p, _i32, _p, _sz, _p]),
     "sig_col_sums": (_i32, [_p, _i64, _i64, _p, _p]),
     "teal_mlp_sparse": (_i32, [_p, _p, _p, _p, _i64, _i64, _f32, _f32, _p, _p, _p, _p, _sz, _p]),
 }
@@ -506,6 +517,168 @@ def nm_act_gemm(X, WT, n: int, m: int, Y=None, ws=None, stream=None):
         _ptr(X), rows, K, _ptr(WT), N, int(n), int(m), _ptr(Y), _ptr(ws), ws.numel(),
         _stream(stream)))
     return Y
+
+
+# Dense products for blocks of tokens.  Their calls run on the tensors' own
+# device, on `stream` or that device's current stream; what they allocate
+# (outputs, and a workspace per call) belongs to that stream, so calls on
+# different streams and captured graphs share nothing.
+
+_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
+def _elsewhere(dev, stream):
+    """None when ``dev`` is the current device and no other stream is asked
+    for; else the context to run in."""
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a CUDA device, got {dev}")
+    if stream is None and dev.index == torch.cuda.current_device():
+        return None
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    if s.device != dev:
+        raise ValueError(f"stream is on {s.device}, the tensors on {dev}")
+    return torch.cuda.stream(s)
+
+
+def _matrix(t, name, like, shape, contiguous=False):
+    """Check a 2-D tensor of ``like``'s type and device; returns its row stride."""
+    if t.dtype != like.dtype or t.device != like.device:
+        raise TypeError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if contiguous:
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return shape[1]
+    if shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    # a single row has no stride of its own: any that the library accepts
+    return t.stride(0) if shape[0] > 1 else -(-shape[1] // 8) * 8
+
+
+def _dense_type(X, name):
+    if X.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {X.dtype}")
+    if X.dim() != 2:
+        raise ValueError(f"{name} must be 2-D (tokens, features)")
+    return _DTYPES[X.dtype]
+
+
+def linear_act(X, WT, bias=None, act: int = ACT_NONE, residual=None, Y=None, stream=None):
+    """Y = act(X WT + bias) + residual for a block of tokens, fp16 or bf16.
+
+    X (rows, K), WT (K, N) contiguous, bias (N,), residual and Y (rows, N);
+    X, residual and Y may have row strides (multiples of 8).  Y may be the
+    residual.  N must be a multiple of 8."""
+    dt = _dense_type(X, "X")
+    ctx = _elsewhere(X.device, stream)
+    if ctx is not None:
+        with ctx:
+            return linear_act(X, WT, bias, act, residual, Y)
+    rows, K = X.shape
+    if WT.dim() != 2:
+        raise ValueError("WT must be 2-D (K, N)")
+    N = WT.shape[1]
+    ldx = _matrix(X, "X", X, (rows, K))
+    _matrix(WT, "WT", X, (K, N), contiguous=True)
+    ldr = 0
+    if bias is not None:
+        if bias.shape != (N,) or bias.dtype != X.dtype or bias.device != X.device or not bias.is_contiguous():
+            raise ValueError(f"bias must be a contiguous {X.dtype} vector of {N} entries on {X.device}")
+    if residual is not None:
+        ldr = _matrix(residual, "residual", X, (rows, N))
+    if Y is None:
+        Y = torch.empty((rows, N), dtype=X.dtype, device=X.device)
+    ldy = _matrix(Y, "Y", X, (rows, N))
+    _check("linear_act", _lib.linear_act(
+        X.data_ptr(), rows, K, ldx, WT.data_ptr(), N, _ptr(bias), int(act), _ptr(residual), ldr,
+        Y.data_ptr(), ldy, dt, _stream()))
+    return Y
+
+
+def gated_mlp(X, WgT, WuT, WdT, act: int = ACT_SILU, residual=None, Y=None, h_out=None, g_out=None,
+              u_out=None, stream=None):
+    """Y = (act(X WgT) . (X WuT)) WdT + residual for a block of tokens, fp16 or bf16.
+
+    X, residual and Y (rows, d_model), row strides allowed; WgT, WuT
+    (d_model, d_ff) and WdT (d_ff, d_model) contiguous.  h_out, g_out and u_out
+    (rows, d_ff) receive the hidden block and the two projections, which
+    gated_mlp_backward takes."""
+    dt = _dense_type(X, "X")
+    ctx = _elsewhere(X.device, stream)
+    if ctx is not None:
+        with ctx:
+            return gated_mlp(X, WgT, WuT, WdT, act, residual, Y, h_out, g_out, u_out)
+    rows, m = X.shape
+    if WgT.dim() != 2:
+        raise ValueError("WgT must be 2-D (d_model, d_ff)")
+    f = WgT.shape[1]
+    ldx = _matrix(X, "X", X, (rows, m))
+    _matrix(WgT, "WgT", X, (m, f), contiguous=True)
+    _matrix(WuT, "WuT", X, (m, f), contiguous=True)
+    _matrix(WdT, "WdT", X, (f, m), contiguous=True)
+    ldr = _matrix(residual, "residual", X, (rows, m)) if residual is not None else 0
+    for name, t in (("h_out", h_out), ("g_out", g_out), ("u_out", u_out)):
+        if t is not None:
+            _matrix(t, name, X, (rows, f), contiguous=True)
+    if Y is None:
+        Y = torch.empty((rows, m), dtype=X.dtype, device=X.device)
+    ldy = _matrix(Y, "Y", X, (rows, m))
+    ws, n = None, 0
+    if h_out is None:
+        n = workspace_bytes(OP_GATED_TOKENS, m, f, rows)
+        ws = torch.empty(n, dtype=torch.uint8, device=X.device)
+    _check("gated_mlp", _lib.gated_mlp(
+        X.data_ptr(), rows, ldx, WgT.data_ptr(), WuT.data_ptr(), WdT.data_ptr(), m, f, int(act),
+        _ptr(residual), ldr, Y.data_ptr(), ldy, _ptr(h_out), _ptr(g_out), _ptr(u_out), dt,
+        _ptr(ws), n, _stream()))
+    return Y
+
+
+def gated_mlp_backward(dY, X, g, u, WgT, WuT, WdT, act: int = ACT_SILU, dX=None, dWgT=None, dWuT=None,
+                       dWdT=None, want_x: bool = True, want_weights: bool = True, stream=None):
+    """Gradients (dX, dWgT, dWuT, dWdT) of gated_mlp from the gradient dY of its
+    output and the g and u that it kept.
+
+    want_x or want_weights False leaves those out (None in their place).  Given
+    gradient tensors are written, not added to."""
+    dt = _dense_type(X, "X")
+    ctx = _elsewhere(X.device, stream)
+    if ctx is not None:
+        with ctx:
+            return gated_mlp_backward(dY, X, g, u, WgT, WuT, WdT, act, dX, dWgT, dWuT, dWdT, want_x,
+                                      want_weights)
+    rows, m = X.shape
+    if WgT.dim() != 2:
+        raise ValueError("WgT must be 2-D (d_model, d_ff)")
+    f = WgT.shape[1]
+    ldx = _matrix(X, "X", X, (rows, m))
+    lddy = _matrix(dY, "dY", X, (rows, m))
+    for name, t, shape in (("g", g, (rows, f)), ("u", u, (rows, f)), ("WgT", WgT, (m, f)),
+                           ("WuT", WuT, (m, f)), ("WdT", WdT, (f, m))):
+        _matrix(t, name, X, shape, contiguous=True)
+    lddx = 0
+    if want_x:
+        if dX is None:
+            dX = torch.empty((rows, m), dtype=X.dtype, device=X.device)
+        lddx = _matrix(dX, "dX", X, (rows, m))
+    else:
+        dX = None
+    if want_weights:
+        dWgT = torch.empty_like(WgT) if dWgT is None else dWgT
+        dWuT = torch.empty_like(WuT) if dWuT is None else dWuT
+        dWdT = torch.empty_like(WdT) if dWdT is None else dWdT
+        for name, t, shape in (("dWgT", dWgT, (m, f)), ("dWuT", dWuT, (m, f)), ("dWdT", dWdT, (f, m))):
+            _matrix(t, name, X, shape, contiguous=True)
+    else:
+        dWgT = dWuT = dWdT = None
+    n = workspace_bytes(OP_GATED_BACKWARD, m, f, rows)
+    ws = torch.empty(n, dtype=torch.uint8, device=X.device)
+    _check("gated_mlp_backward", _lib.gated_mlp_backward(
+        dY.data_ptr(), lddy, X.data_ptr(), ldx, rows, g.data_ptr(), u.data_ptr(), WgT.data_ptr(),
+        WuT.data_ptr(), WdT.data_ptr(), m, f, int(act), _ptr(dX), lddx, _ptr(dWgT), _ptr(dWuT),
+        _ptr(dWdT), dt, ws.data_ptr(), n, _stream()))
+    return dX, dWgT, dWuT, dWdT
 
 
 def take_device_error(stream=None) -> int:

@@ -3,12 +3,14 @@
 // a check fails; otherwise it enqueues its kernels on the caller's stream and
 // returns at once.
 #include "../../include/sig.h"
+#include "dense.h"
 #include "internal.h"
 #include "nm_ex.h"
 
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 using namespace sig;
 
@@ -33,6 +35,30 @@ size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 bool nm_pattern_ok(int n, int m) {
   const bool pow2 = m == 1 || m == 2 || m == 4 || m == 8 || m == 16 || m == 32;
   return pow2 && n >= 1 && n <= m;
+}
+
+// Dense products for blocks of tokens: sizes, strides and alignment.
+constexpr int64_t kMaxRows = 1 << 24, kMaxWidth = 1 << 20, kMaxStride = 1 << 30;
+
+bool dense_width(int64_t n) { return n >= 8 && n % 8 == 0 && n <= kMaxWidth; }
+size_t hidden_bytes(int64_t rows, int64_t d_ff) {
+  return round_up((size_t)rows * (size_t)d_ff * 2, 256);
+}
+bool dense_args(int dtype, int act) {
+  return (dtype == SIG_F16 || dtype == SIG_BF16) && act >= SIG_ACT_NONE && act <= SIG_ACT_SILU;
+}
+
+// SHAPE or ALIGN for a row-strided buffer of `width` entries a row; NULL passes.
+int check_rows(const void* p, int64_t ld, int64_t width) {
+  if (p == nullptr) return SIG_OK;
+  if (ld < width || ld > kMaxStride) return SIG_ERR_SHAPE;
+  return ld % 8 == 0 && aligned16(p) ? SIG_OK : SIG_ERR_ALIGN;
+}
+
+int first_error(std::initializer_list<int> checks) {
+  for (int c : checks)
+    if (c != SIG_OK) return c;
+  return SIG_OK;
 }
 
 }  // namespace
@@ -83,6 +109,10 @@ size_t sig_workspace_bytes(int op, int64_t d_in, int64_t d_out, int64_t rows) {
     case SIG_OP_NM_GEMM:
       if (rows < 1 || d_in < 1) return 0;
       return round_up((size_t)rows * (size_t)d_in * 2, 256);   // the masked activation block
+    case SIG_OP_GATED_TOKENS:     // h
+    case SIG_OP_GATED_BACKWARD:   // dg, du, h
+      if (rows < 1 || rows > kMaxRows || !dense_width(d_in) || !dense_width(d_out)) return 0;
+      return (op == SIG_OP_GATED_TOKENS ? 1 : 3) * hidden_bytes(rows, d_out);
   }
   return 0;
 }
@@ -444,16 +474,160 @@ int nm_act_gemm_packed(const void* packed, int64_t rows, int64_t K, const uint16
                                     (cudaStream_t)stream));
 }
 
+int linear_act(const uint16_t* X, int64_t rows, int64_t K, int64_t ldx, const uint16_t* WT,
+               int64_t N, const uint16_t* bias, int act, const uint16_t* residual, int64_t ldr,
+               uint16_t* Y, int64_t ldy, int dtype, sig_stream_t stream) {
+  if (!dense_args(dtype, act)) return SIG_ERR_ARG;
+  if (rows < 0 || rows > kMaxRows || K < 1 || K > kMaxWidth || !dense_width(N)) return SIG_ERR_SHAPE;
+  if (rows == 0) return SIG_OK;   // an empty block: nothing to read or write
+  if (X == nullptr || WT == nullptr || Y == nullptr) return SIG_ERR_NULL;
+  const int bad = first_error(
+      {check_rows(X, ldx, K), check_rows(residual, ldr, N), check_rows(Y, ldy, N)});
+  if (bad != SIG_OK) return bad;
+  if (!aligned16(WT) || !aligned16(bias)) return SIG_ERR_ALIGN;
+  DenseGemm d;
+  d.bf16 = dtype == SIG_BF16;
+  d.rows = rows; d.cols = N; d.K = K;
+  d.a[0] = X; d.lda = ldx;
+  d.b[0] = WT; d.ldb = N;
+  d.act = act; d.bias = bias; d.residual = residual; d.ldr = ldr;
+  d.o[0] = Y; d.ldo = ldy;
+  return cuda_status(launch_dense(d, (cudaStream_t)stream));
+}
+
+int gated_mlp(const uint16_t* X, int64_t rows, int64_t ldx, const uint16_t* WgT,
+              const uint16_t* WuT, const uint16_t* WdT, int64_t d_model, int64_t d_ff, int act,
+              const uint16_t* residual, int64_t ldr, uint16_t* Y, int64_t ldy, uint16_t* h_out,
+              uint16_t* g_out, uint16_t* u_out, int dtype, void* ws, size_t ws_bytes,
+              sig_stream_t stream) {
+  if (!dense_args(dtype, act)) return SIG_ERR_ARG;
+  if (rows < 0 || rows > kMaxRows || !dense_width(d_model) || !dense_width(d_ff))
+    return SIG_ERR_SHAPE;
+  if (rows == 0) return SIG_OK;
+  if (X == nullptr || WgT == nullptr || WuT == nullptr || WdT == nullptr || Y == nullptr ||
+      (g_out == nullptr) != (u_out == nullptr))
+    return SIG_ERR_NULL;
+  const int bad = first_error({check_rows(X, ldx, d_model), check_rows(residual, ldr, d_model),
+                               check_rows(Y, ldy, d_model)});
+  if (bad != SIG_OK) return bad;
+  if (!aligned16(WgT) || !aligned16(WuT) || !aligned16(WdT) || !aligned16(h_out) ||
+      !aligned16(g_out) || !aligned16(u_out))
+    return SIG_ERR_ALIGN;
+  if (h_out == nullptr) {
+    if (ws == nullptr || ws_bytes < hidden_bytes(rows, d_ff)) return SIG_ERR_WORKSPACE;
+    if (!aligned256(ws)) return SIG_ERR_ALIGN;
+  }
+  uint16_t* h = h_out != nullptr ? h_out : static_cast<uint16_t*>(ws);
+
+  DenseGemm up;
+  up.epi = DENSE_GATED;
+  up.bf16 = dtype == SIG_BF16;
+  up.rows = rows; up.cols = d_ff; up.K = d_model;
+  up.a[0] = X; up.lda = ldx;
+  up.b[0] = WgT; up.b[1] = WuT; up.ldb = d_ff;
+  up.act = act;
+  up.o[0] = h; up.o[1] = g_out; up.o[2] = u_out; up.ldo = d_ff;
+  if (launch_dense(up, (cudaStream_t)stream) != cudaSuccess) return SIG_ERR_CUDA;
+
+  DenseGemm dn;
+  dn.bf16 = up.bf16;
+  dn.rows = rows; dn.cols = d_model; dn.K = d_ff;
+  dn.a[0] = h; dn.lda = d_ff;
+  dn.b[0] = WdT; dn.ldb = d_model;
+  dn.residual = residual; dn.ldr = ldr;
+  dn.o[0] = Y; dn.ldo = ldy;
+  return cuda_status(launch_dense(dn, (cudaStream_t)stream));
+}
+
+int gated_mlp_backward(const uint16_t* dY, int64_t lddy, const uint16_t* X, int64_t ldx,
+                       int64_t rows, const uint16_t* g, const uint16_t* u, const uint16_t* WgT,
+                       const uint16_t* WuT, const uint16_t* WdT, int64_t d_model, int64_t d_ff,
+                       int act, uint16_t* dX, int64_t lddx, uint16_t* dWgT, uint16_t* dWuT,
+                       uint16_t* dWdT, int dtype, void* ws, size_t ws_bytes, sig_stream_t stream) {
+  if (!dense_args(dtype, act)) return SIG_ERR_ARG;
+  if (rows < 0 || rows > kMaxRows || !dense_width(d_model) || !dense_width(d_ff))
+    return SIG_ERR_SHAPE;
+  if ((dWgT == nullptr) != (dWuT == nullptr) ||
+      (dX == nullptr && dWgT == nullptr && dWdT == nullptr))
+    return SIG_ERR_NULL;
+  if (!aligned16(dWgT) || !aligned16(dWuT) || !aligned16(dWdT)) return SIG_ERR_ALIGN;
+  cudaStream_t st = (cudaStream_t)stream;
+  if (rows == 0) {   // no tokens: the weight gradients are zero
+    for (uint16_t* w : {dWgT, dWuT, dWdT})
+      if (w != nullptr &&
+          cudaMemsetAsync(w, 0, (size_t)d_model * (size_t)d_ff * 2, st) != cudaSuccess)
+        return SIG_ERR_CUDA;
+    return SIG_OK;
+  }
+  if (dY == nullptr || X == nullptr || g == nullptr || u == nullptr || WgT == nullptr ||
+      WuT == nullptr || WdT == nullptr)
+    return SIG_ERR_NULL;
+  const int bad = first_error({check_rows(dY, lddy, d_model), check_rows(X, ldx, d_model),
+                               check_rows(dX, lddx, d_model)});
+  if (bad != SIG_OK) return bad;
+  if (!aligned16(g) || !aligned16(u) || !aligned16(WgT) || !aligned16(WuT) || !aligned16(WdT))
+    return SIG_ERR_ALIGN;
+  const size_t hb = hidden_bytes(rows, d_ff);
+  if (ws == nullptr || ws_bytes < 3 * hb) return SIG_ERR_WORKSPACE;
+  if (!aligned256(ws)) return SIG_ERR_ALIGN;
+  uint16_t* dg = static_cast<uint16_t*>(ws);
+  uint16_t* du = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + hb);
+  uint16_t* h = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + 2 * hb);
+  const bool bf16 = dtype == SIG_BF16;
+
+  DenseGemm dh;   // dh = dY WdT^T; dg, du and h from it, g and u
+  dh.epi = DENSE_GRAD;
+  dh.bf16 = bf16;
+  dh.rows = rows; dh.cols = d_ff; dh.K = d_model;
+  dh.a[0] = dY; dh.lda = lddy;
+  dh.b_k = true; dh.b[0] = WdT; dh.ldb = d_model;
+  dh.act = act; dh.g = g; dh.u = u;
+  dh.o[0] = dg; dh.o[1] = du; dh.o[2] = h; dh.ldo = d_ff;
+  if (launch_dense(dh, st) != cudaSuccess) return SIG_ERR_CUDA;
+
+  if (dX != nullptr) {   // dX = dg WgT^T + du WuT^T, one sum over both
+    DenseGemm x;
+    x.bf16 = bf16;
+    x.rows = rows; x.cols = d_model; x.K = d_ff;
+    x.two_segments = true;
+    x.a[0] = dg; x.a[1] = du; x.lda = d_ff;
+    x.b_k = true; x.b[0] = WgT; x.b[1] = WuT; x.ldb = d_ff;
+    x.o[0] = dX; x.ldo = lddx;
+    if (launch_dense(x, st) != cudaSuccess) return SIG_ERR_CUDA;
+  }
+  if (dWgT != nullptr) {   // dWgT = X^T dg and dWuT = X^T du, one launch
+    DenseGemm w;
+    w.bf16 = bf16;
+    w.rows = d_model; w.cols = d_ff; w.K = rows;
+    w.a_mn = true; w.a[0] = X; w.lda = ldx;
+    w.mats = 2; w.b[0] = dg; w.b[1] = du; w.ldb = d_ff;
+    w.o[0] = dWgT; w.o[1] = dWuT; w.ldo = d_ff;
+    if (launch_dense(w, st) != cudaSuccess) return SIG_ERR_CUDA;
+  }
+  if (dWdT != nullptr) {   // dWdT = h^T dY
+    DenseGemm w;
+    w.bf16 = bf16;
+    w.rows = d_ff; w.cols = d_model; w.K = rows;
+    w.a_mn = true; w.a[0] = h; w.lda = d_ff;
+    w.b[0] = dY; w.ldb = lddy;
+    w.o[0] = dWdT; w.ldo = d_model;
+    if (launch_dense(w, st) != cudaSuccess) return SIG_ERR_CUDA;
+  }
+  return SIG_OK;
+}
+
 int sig_set_wait_limit(long long cycles) {
-  return cuda_status(set_wait_limit(cycles));
+  if (set_wait_limit(cycles) != cudaSuccess) return SIG_ERR_CUDA;
+  return cuda_status(set_dense_wait_limit(cycles));
 }
 
 int sig_take_device_error(unsigned* code, sig_stream_t stream) {
   if (code == nullptr) return SIG_ERR_NULL;
-  unsigned gemm = 0, gemv = 0;
+  unsigned gemm = 0, gemv = 0, dense = 0;
   if (read_device_error(&gemm, (cudaStream_t)stream) != cudaSuccess) return SIG_ERR_CUDA;
   if (read_gemv_error(&gemv, (cudaStream_t)stream) != cudaSuccess) return SIG_ERR_CUDA;
-  *code = gemm | gemv;
+  if (read_dense_error(&dense, (cudaStream_t)stream) != cudaSuccess) return SIG_ERR_CUDA;
+  *code = gemm | gemv | dense;
   return *code == 0u ? SIG_OK : SIG_ERR_TIMEOUT;
 }
 
