@@ -526,14 +526,19 @@ def nm_act_gemm(X, WT, n: int, m: int, Y=None, ws=None, stream=None):
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 
+# The handle of a device's current stream: torch's own accessor, which a small
+# call cannot afford to wrap in a Stream object, where this build has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
 
 def _elsewhere(dev, stream):
     """None when ``dev`` is the current device and no other stream is asked
     for; else the context to run in."""
+    if stream is None and dev.index is not None and dev.index == torch.cuda.current_device():
+        return None
     if dev.type != "cuda":
         raise ValueError(f"tensors must be on a CUDA device, got {dev}")
-    if stream is None and dev.index == torch.cuda.current_device():
-        return None
     s = stream if stream is not None else torch.cuda.current_stream(dev)
     if s.device != dev:
         raise ValueError(f"stream is on {s.device}, the tensors on {dev}")
@@ -542,7 +547,7 @@ def _elsewhere(dev, stream):
 
 def _matrix(t, name, like, shape, contiguous=False):
     """Check a 2-D tensor of ``like``'s type and device; returns its row stride."""
-    if t.dtype != like.dtype or t.device != like.device:
+    if t is not like and (t.dtype != like.dtype or t.device != like.device):
         raise TypeError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -588,11 +593,12 @@ def linear_act(X, WT, bias=None, act: int = ACT_NONE, residual=None, Y=None, str
     if residual is not None:
         ldr = _matrix(residual, "residual", X, (rows, N))
     if Y is None:
-        Y = torch.empty((rows, N), dtype=X.dtype, device=X.device)
-    ldy = _matrix(Y, "Y", X, (rows, N))
+        Y, ldy = X.new_empty((rows, N)), N
+    else:
+        ldy = _matrix(Y, "Y", X, (rows, N))
     _check("linear_act", _lib.linear_act(
         X.data_ptr(), rows, K, ldx, WT.data_ptr(), N, _ptr(bias), int(act), _ptr(residual), ldr,
-        Y.data_ptr(), ldy, dt, _stream()))
+        Y.data_ptr(), ldy, dt, _raw_stream(X.device.index)))
     return Y
 
 
@@ -622,16 +628,17 @@ def gated_mlp(X, WgT, WuT, WdT, act: int = ACT_SILU, residual=None, Y=None, h_ou
         if t is not None:
             _matrix(t, name, X, (rows, f), contiguous=True)
     if Y is None:
-        Y = torch.empty((rows, m), dtype=X.dtype, device=X.device)
-    ldy = _matrix(Y, "Y", X, (rows, m))
+        Y, ldy = X.new_empty((rows, m)), m
+    else:
+        ldy = _matrix(Y, "Y", X, (rows, m))
     ws, n = None, 0
     if h_out is None:
         n = workspace_bytes(OP_GATED_TOKENS, m, f, rows)
-        ws = torch.empty(n, dtype=torch.uint8, device=X.device)
+        ws = X.new_empty(n, dtype=torch.uint8)
     _check("gated_mlp", _lib.gated_mlp(
         X.data_ptr(), rows, ldx, WgT.data_ptr(), WuT.data_ptr(), WdT.data_ptr(), m, f, int(act),
         _ptr(residual), ldr, Y.data_ptr(), ldy, _ptr(h_out), _ptr(g_out), _ptr(u_out), dt,
-        _ptr(ws), n, _stream()))
+        _ptr(ws), n, _raw_stream(X.device.index)))
     return Y
 
 
@@ -660,7 +667,7 @@ def gated_mlp_backward(dY, X, g, u, WgT, WuT, WdT, act: int = ACT_SILU, dX=None,
     lddx = 0
     if want_x:
         if dX is None:
-            dX = torch.empty((rows, m), dtype=X.dtype, device=X.device)
+            dX = X.new_empty((rows, m))
         lddx = _matrix(dX, "dX", X, (rows, m))
     else:
         dX = None
@@ -673,11 +680,11 @@ def gated_mlp_backward(dY, X, g, u, WgT, WuT, WdT, act: int = ACT_SILU, dX=None,
     else:
         dWgT = dWuT = dWdT = None
     n = workspace_bytes(OP_GATED_BACKWARD, m, f, rows)
-    ws = torch.empty(n, dtype=torch.uint8, device=X.device)
+    ws = X.new_empty(n, dtype=torch.uint8)
     _check("gated_mlp_backward", _lib.gated_mlp_backward(
         dY.data_ptr(), lddy, X.data_ptr(), ldx, rows, g.data_ptr(), u.data_ptr(), WgT.data_ptr(),
         WuT.data_ptr(), WdT.data_ptr(), m, f, int(act), _ptr(dX), lddx, _ptr(dWgT), _ptr(dWuT),
-        _ptr(dWdT), dt, ws.data_ptr(), n, _stream()))
+        _ptr(dWdT), dt, ws.data_ptr(), n, _raw_stream(X.device.index)))
     return dX, dWgT, dWuT, dWdT
 
 

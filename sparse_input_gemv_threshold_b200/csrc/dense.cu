@@ -2,12 +2,15 @@
 // gate and up projections of a gated MLP with the activation and the product
 // of the two in the epilogue, and the products of its backward pass.
 //
-// Two kernels.  dense_pair_kernel is persistent: one CTA pair per SM pair
-// walks 256 x 256 output tiles with two accumulators in tensor memory, so the
-// epilogue of a tile runs beside the mainloop of the next.
-// dense_split_kernel serves small blocks of tokens: one 128 x BN tile per
-// cluster, the cluster's CTAs each taking a part of K and joining their
-// sums through distributed shared memory in a fixed order.
+//   dense_pair_kernel  persistent: CTA pairs walk tiles of 256 tokens x 128 or
+//                      256 columns with two accumulators in tensor memory, so
+//                      the epilogue of a tile runs beside the mainloop of the next.
+//   dense_few_kernel   few tokens, bound by reading the weight: the weight is the
+//                      MMA's M operand (128 of its columns, one a tensor-memory
+//                      lane) and the tokens its N operand; one tile per cluster,
+//                      whose CTAs each take a part of K and join their float32
+//                      sums through distributed shared memory in a fixed order:
+//                      no workspace, no atomics, the same bits in every run.
 #include "common.cuh"
 #include "dense.h"
 #include "internal.h"
@@ -36,9 +39,9 @@ struct DenseMaps {
 };
 
 struct DenseArgs {
-  int rows, cols;      // of one output
+  int rows, cols;      // rows (tokens) and columns of one output
   int kb0, kbt;        // K stages of the first segment, of both
-  int tm, tn;          // tiles down and across (of one weight)
+  int tm, tn;          // tiles down, and across one weight
   int mats;
   int outs;            // outputs to store (DENSE_GATED: 1, or 3 with g and u)
   int act;
@@ -65,11 +68,30 @@ __device__ __forceinline__ bool try_cluster(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
-__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  if (try_cluster(bar, parity)) return true;
+// The limit of this launch's waits, read once: a load in every wait that does
+// not succeed at once would add its latency to the stage.
+__device__ __forceinline__ long long wait_limit() { return *(volatile long long*)&g_dense_wait_limit; }
+
+// The same without the hardware's own suspension, which may outlast a short limit.
+__device__ __forceinline__ bool poll_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+constexpr long long kShortLimit = 1 << 20;   // cycles: shorter limits are polled
+
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                             long long limit) {
+  if (poll_cluster(bar, parity)) return true;
   const long long t0 = clock64();
-  const long long limit = *(volatile long long*)&g_dense_wait_limit;
-  while (!try_cluster(bar, parity)) {
+  while (!(limit < kShortLimit ? poll_cluster(bar, parity) : try_cluster(bar, parity))) {
     if (*abort_flag) return false;
     if (clock64() - t0 > limit) {
       *abort_flag = 1;
@@ -93,6 +115,11 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
                : "memory");
 }
 
+// Bring a tensor map (a kernel argument) into the descriptor cache.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // ---------------------------------------------------------------------------
 // Descriptors
 // ---------------------------------------------------------------------------
@@ -103,12 +130,35 @@ __host__ __device__ constexpr uint32_t dense_idesc(int M, int N, bool bf16, bool
          ((b_k ? 0u : 1u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Shared-memory descriptor of K step k (16 values) of an operand slab.
-// K-major: rows of 128 bytes, the step 32 bytes into each; MN-major: blocks of
-// 64 columns x 64 k-rows (kBlock bytes apart), the step 16 k-rows down.
+// Shared-memory descriptor of an operand slab, in its two words (see
+// smem_desc): the low one holds the address and the leading offset, the high
+// one is constant.  K-major: rows of 128 bytes; MN-major: blocks of 64 columns
+// x 64 k-rows, kBlock bytes apart.  A K step of 16 values is 32 bytes into the
+// rows, or 16 k-rows down: slab_step in the address's 16-byte units.  The
+// issuing thread only adds to the low word; building each descriptor in full
+// took longer than the MMAs of the stage: 0.30 against 0.19 us a stage of 128
+// columns at 256 x 8192 x 256 on B200.
 template <bool MN>
-__device__ __forceinline__ uint64_t slab_desc(uint32_t base, int k) {
-  return MN ? smem_desc(base + k * 2048, kBlock, 1024) : smem_desc(base + k * 32, 16, 1024);
+__device__ __forceinline__ uint32_t slab_low(uint32_t addr) {
+  // the address within the CTA: a cluster rank sits above it in the shared window
+  return ((addr >> 4) & 0x3fffu) | ((MN ? kBlock >> 4 : 1u) << 16);
+}
+constexpr uint32_t kSlabHigh = (1024u >> 4) | (1u << 14) | (2u << 29);   // 8-row groups, version, swizzle
+template <bool MN>
+constexpr uint32_t slab_step = MN ? 2048u >> 4 : 32u >> 4;
+
+__device__ __forceinline__ uint64_t slab_desc(uint32_t low) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(low), "r"(kSlabHigh));
+  return d;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 template <int GROUP>
@@ -240,6 +290,183 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 
 __device__ __forceinline__ uint4 ld16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
+// What the epilogue of 8 columns of a token reads besides the sums: the
+// residual, or g and u.  Loaded ahead of the sums.
+struct Extra {
+  uint4 x, y;
+};
+
+template <int EPI>
+__device__ __forceinline__ Extra load_extra(const DenseArgs& a, int row, int col) {
+  Extra e = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (row >= a.rows || col >= a.cols) return e;
+  if constexpr (EPI == DENSE_LINEAR) {
+    if (a.residual != nullptr)   // a plain load: Y may be the residual buffer itself
+      e.x = *reinterpret_cast<const uint4*>(a.residual + (int64_t)row * a.ldr + col);
+  } else if constexpr (EPI == DENSE_GRAD) {
+    const int64_t at = (int64_t)row * a.cols + col;
+    e.x = ld16(a.g + at);
+    e.y = ld16(a.u + at);
+  }
+  return e;
+}
+
+__device__ __forceinline__ void store16(uint16_t* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
+
+// The outputs of 8 columns of a token from its float32 sums v (DENSE_GATED: g
+// in v and u in w).
+template <int EPI, bool BF>
+__device__ __forceinline__ void finish8(float (&v)[8], const float (&w)[8], const Extra& e,
+                                        const DenseArgs& a, int mat, int row, int col) {
+  const int64_t at = (int64_t)row * a.ldo + col;
+  if constexpr (EPI == DENSE_LINEAR) {
+    if (a.bias != nullptr) {
+      float b[8];
+      unpack8<BF>(b, ld16(a.bias + col));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += b[i];
+    }
+    if (a.act != SIG_ACT_NONE)
+      with_act(a.act, [&](auto A) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = act_value<decltype(A)::value>(v[i], act_share<decltype(A)::value>(v[i]));
+      });
+    if (a.residual != nullptr) {
+      float r[8];
+      unpack8<BF>(r, e.x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] += r[i];
+    }
+    store16(a.o[mat] + at, pack8<BF>(v));
+  } else if constexpr (EPI == DENSE_GATED) {
+    if (a.outs == 3) {
+      store16(a.o[1] + at, pack8<BF>(v));
+      store16(a.o[2] + at, pack8<BF>(w));
+    }
+    with_act(a.act, [&](auto A) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = act_value<decltype(A)::value>(v[i], act_share<decltype(A)::value>(v[i])) * w[i];
+    });
+    store16(a.o[0] + at, pack8<BF>(v));
+  } else {
+    float g[8], u[8], dg[8], du[8], h[8];
+    unpack8<BF>(g, e.x);
+    unpack8<BF>(u, e.y);
+    with_act(a.act, [&](auto A) {
+      constexpr int ACT = decltype(A)::value;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float p = act_share<ACT>(g[i]), y = act_value<ACT>(g[i], p);
+        dg[i] = v[i] * u[i] * act_slope<ACT>(g[i], p);
+        du[i] = v[i] * y;
+        h[i] = y * u[i];
+      }
+    });
+    store16(a.o[0] + at, pack8<BF>(dg));
+    store16(a.o[1] + at, pack8<BF>(du));
+    store16(a.o[2] + at, pack8<BF>(h));
+  }
+}
+
+// 16 tensor-memory columns (tokens) of this warp's 32 lanes
+__device__ __forceinline__ void tmem_ld16(float (&v)[16], uint32_t addr) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
+// The join of `parts` CTAs that split K.  Part j joins tokens [j own, (j + 1)
+// own) of the tile.  join_send: eight warps send this CTA's sums of every
+// token to the part that joins it, at [part][token - j own][128 columns] of its
+// buffer; `cta(j)` is part j's rank in the cluster.  A warp's 32 lanes write
+// 128 contiguous bytes, the two warps of a lane quarter take groups of 16
+// tokens in turn.
+template <typename F>
+__device__ __forceinline__ void join_send(uint32_t buf, uint32_t acc, int warp, int lane, int valid,
+                                          int own, int part, F&& cta) {
+  const int q = warp & 3;
+  const uint32_t base = buf + (uint32_t)((part * own * 128 + q * 32 + lane) * 4);
+#pragma unroll 1
+  for (int c = (warp >> 2) * 16; c < valid; c += 32) {
+    float v[16];
+    tmem_ld16(v, acc + ((uint32_t)(q * 32) << 16) + (uint32_t)c);
+    int owner = c / own, slot = c - owner * own;
+    uint32_t to = map_to_rank(base, cta(owner)) + (uint32_t)slot * 512u;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (c + i < valid) {
+        st_cluster_f32(to, v[i]);
+        to += 512u;
+        if (++slot == own && c + i + 1 < valid) {
+          slot = 0;
+          to = map_to_rank(base, cta(++owner));
+        }
+      }
+  }
+}
+
+// Adds the parts in order and finishes the tokens of `part`; 256 threads.
+// n0 is the CTA's first output column, t0 the tile's first token.
+template <int EPI, bool BF>
+__device__ __forceinline__ void join_finish(const uint8_t* buf, const DenseArgs& args, int mat, int n0,
+                                            int t0, int valid, int own, int part, int parts) {
+  constexpr int kChunks = EPI == DENSE_GATED ? 8 : 16;   // 8-column chunks of a token
+  const int mine = min(own, valid - part * own);         // may be negative: nothing to join
+  for (int i = threadIdx.x; i < mine * kChunks; i += 256) {
+    const int slot = i / kChunks, ch = i % kChunks;
+    const int row = t0 + part * own + slot, col = n0 + ch * 8;
+    if (col >= args.cols) continue;
+    const Extra e = load_extra<EPI>(args, row, col);
+    auto gather = [&](float (&v)[8], int first) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = 0.f;
+      for (int src = 0; src < parts; ++src) {
+        const float4* f =
+            reinterpret_cast<const float4*>(buf + (size_t)((src * own + slot) * 128 + first) * 4);
+        const float4 a = f[0], b = f[1];
+        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+      }
+    };
+    float v[8], w[8] = {};
+    gather(v, ch * 8);
+    if constexpr (EPI == DENSE_GATED) gather(w, 64 + ch * 8);
+    finish8<EPI, BF>(v, w, e, args, mat, row, col);
+  }
+}
+
+// The weight's boxes of K stage kb for a CTA's 128 accumulator lanes from
+// output column n0: each(map, coordinates, byte offset in the operand).
+template <bool B_K, int EPI, typename F>
+__device__ __forceinline__ void weight_boxes(const DenseMaps& maps, const DenseArgs& args, int mat, int n0,
+                                             int kb, F&& each) {
+  const int seg = kb >= args.kb0 ? 1 : 0;
+  const int k = (kb - (seg ? args.kb0 : 0)) * kSlab;
+  if constexpr (B_K) {
+    each(&maps.b[seg | mat], k, n0, 0u);
+  } else if constexpr (EPI == DENSE_GATED) {   // 64 columns of each weight: lanes 0 .. 63 g, 64 .. 127 u
+    each(&maps.b[0], n0, k, 0u);
+    each(&maps.b[1], n0, k, kBlock);
+  } else {
+    each(&maps.b[seg | mat], n0, k, 0u);
+    each(&maps.b[seg | mat], n0 + 64, k, kBlock);
+  }
+}
+
 // v[0 .. 8 G) = act(v + bias) + residual for 8 G columns from `col` of `row`;
 // columns from `cols` on and rows from `rows` on are left without the two.
 template <bool BF, int G>
@@ -310,25 +537,30 @@ __device__ __forceinline__ void epi_grad8(const float* dh, const uint4& gv, cons
 }
 
 // ---------------------------------------------------------------------------
-// Persistent CTA-pair kernel, 256 x 256 tiles
+// Persistent CTA pairs: tiles of 256 tokens x 128 or 256 accumulator columns
 // ---------------------------------------------------------------------------
-constexpr int kPairStages = 6;
 constexpr int kPairThreads = 320;                  // 8 epilogue warps, one loads, one issues MMAs
+constexpr int kPairMaxStages = 8;
 constexpr uint32_t kOperand = kTile * kSlab * 2;   // 16 KB: 128 rows (or columns) x 64 K
-constexpr uint32_t kPairStageBytes = 2 * kOperand;
+constexpr uint32_t kStoreBlock = 32 * 128;         // per epilogue warp: 32 rows x 64 columns
 constexpr int kGroupRows = 8;                      // row tiles walked together (L2 reuse of B)
+constexpr int kSmemPerCta = 227 * 1024;
 
-struct __align__(1024) PairShared {
-  uint8_t A[kPairStages][kOperand];
-  uint8_t B[kPairStages][kOperand];
-  uint8_t stage[8][4096];                          // per epilogue warp: 32 rows x 64 columns
-  unsigned long long full[kPairStages];            // used in the leader
-  unsigned long long empty[kPairStages];
+// After the ring (stage: 128 rows of A, then this CTA's half of the columns
+// of B) and the eight epilogue warps' store blocks.
+struct PairBars {
+  unsigned long long full[kPairMaxStages];         // used in the leader
+  unsigned long long empty[kPairMaxStages];
   unsigned long long acc_full[2], acc_empty[2];    // acc_empty used in the leader
   unsigned long long done;
   uint32_t tmem_base;
   int abort_flag;
   int consumed;
+};
+
+struct PairShape {
+  int bn;        // accumulator columns of a tile: 128 or 256
+  int stages;
 };
 
 struct TilePos {
@@ -371,11 +603,16 @@ __device__ __forceinline__ void stage_store(uint32_t stage, int lane, const CUte
 }
 
 template <bool A_MN, bool B_K, int EPI, bool BF>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__ DenseArgs args) {
+__global__ void __launch_bounds__(kPairThreads, 1)
+dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__ DenseArgs args,
+                  const PairShape ps) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  PairShared& sm = *reinterpret_cast<PairShared*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const int S = ps.stages, bn = ps.bn;
+  const uint32_t stage_bytes = kOperand + (uint32_t)bn * 64u;
+  uint8_t* blocks = ring + (size_t)S * stage_bytes;
+  PairBars& sm = *reinterpret_cast<PairBars*>(blocks + 8 * kStoreBlock);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
@@ -384,8 +621,10 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
   volatile int* abort_flag = &sm.abort_flag;
   pdl_trigger();
 
+  if (warp == 9 && lane < 7)
+    prefetch_map(lane < 2 ? &maps.a[lane] : lane < 4 ? &maps.b[lane - 2] : &maps.o[lane - 4]);
   if (tid == 0) {
-    for (int s = 0; s < kPairStages; ++s) {
+    for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&sm.full[s]), 1);
       mbar_init(smem_u32(&sm.empty[s]), 1);
     }
@@ -411,76 +650,92 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = sm.tmem_base;
   pdl_wait();
+  const long long limit = wait_limit();
 
   int issued = 0;   // stages whose copies this CTA's producer has issued
-  if (warp == 8) {
-    if (lane == 0) {   // ---- TMA producer (both CTAs) ----
-      for (int t = pair; t < tiles && !*abort_flag; t += pairs) {
-        const TilePos p = tile_at(t, args.tm, tn_all);
-        const int m0 = p.m * 256 + (int)rank * 128;
-        const int mat = p.n / args.tn, nt = p.n - mat * args.tn;
-        const int nb = EPI == DENSE_GATED ? nt * 128 : nt * 256 + (int)rank * 128;
-        for (int kb = 0; kb < args.kbt; ++kb) {
-          const int s = issued % kPairStages;
-          const uint32_t ph = (uint32_t)(issued / kPairStages) & 1u;
-          if (!wait_bounded(smem_u32(&sm.empty[s]), ph ^ 1u, abort_flag)) break;
-          const int seg = kb >= args.kb0 ? 1 : 0;
-          const int k = (kb - (seg ? args.kb0 : 0)) * kSlab;
-          const CUtensorMap* ma = &maps.a[seg];
-          const CUtensorMap* mb = &maps.b[EPI == DENSE_GATED ? (int)rank : seg | mat];
-          const uint32_t fb = map_to_rank(smem_u32(&sm.full[s]), 0);
-          if (leader) mbar_expect_tx(smem_u32(&sm.full[s]), 2 * kPairStageBytes);
+  if (warp == 8) {   // ---- TMA producer (both CTAs): the warp loops, one lane issues ----
+    int s = 0;
+    uint32_t ph = 1;
+    bool go = true;
+    const uint32_t full0 = map_to_rank(smem_u32(&sm.full[0]), 0);
+    for (int t = pair; t < tiles && go; t += pairs) {
+      const TilePos p = tile_at(t, args.tm, tn_all);
+      const int m0 = p.m * 256 + (int)rank * 128;
+      const int mat = p.n / args.tn, nt = p.n - mat * args.tn;
+      // DENSE_GATED: CTA 0 brings the gate's columns, CTA 1 the up's
+      const int nb = EPI == DENSE_GATED ? nt * (bn / 2) : nt * bn + (int)rank * (bn / 2);
+      for (int kb = 0; kb < args.kbt; ++kb) {
+        go = __all_sync(kFull, wait_bounded(smem_u32(&sm.empty[s]), ph, abort_flag, limit));
+        if (!go) break;
+        const int seg = kb >= args.kb0 ? 1 : 0;
+        const int k = (kb - (seg ? args.kb0 : 0)) * kSlab;
+        const CUtensorMap* ma = &maps.a[seg];
+        const CUtensorMap* mb = &maps.b[EPI == DENSE_GATED ? (int)rank : seg | mat];
+        const uint32_t fb = full0 + (uint32_t)s * 8u;
+        const uint32_t a0 = smem_u32(ring) + (uint32_t)s * stage_bytes, b0 = a0 + kOperand;
+        if (elect_one()) {
+          if (leader) mbar_expect_tx(smem_u32(&sm.full[s]), 2 * stage_bytes);
           if constexpr (A_MN) {
-            tma_load_2d_pair(smem_u32(sm.A[s]), ma, m0, k, fb);
-            tma_load_2d_pair(smem_u32(sm.A[s]) + kBlock, ma, m0 + 64, k, fb);
+            tma_load_2d_pair(a0, ma, m0, k, fb);
+            tma_load_2d_pair(a0 + kBlock, ma, m0 + 64, k, fb);
           } else {
-            tma_load_2d_pair(smem_u32(sm.A[s]), ma, k, m0, fb);
+            tma_load_2d_pair(a0, ma, k, m0, fb);
           }
           if constexpr (B_K) {
-            tma_load_2d_pair(smem_u32(sm.B[s]), mb, k, nb, fb);
+            tma_load_2d_pair(b0, mb, k, nb, fb);
           } else {
-            tma_load_2d_pair(smem_u32(sm.B[s]), mb, nb, k, fb);
-            tma_load_2d_pair(smem_u32(sm.B[s]) + kBlock, mb, nb + 64, k, fb);
+            tma_load_2d_pair(b0, mb, nb, k, fb);
+            if (bn == 256) tma_load_2d_pair(b0 + kBlock, mb, nb + 64, k, fb);
           }
-          ++issued;
         }
+        __syncwarp();
+        ++issued;
+        if (++s == S) { s = 0; ph ^= 1u; }
       }
     }
-    __syncwarp();
-  } else if (warp == 9) {
-    if (leader && lane == 0) {   // ---- MMA issuer ----
-      constexpr uint32_t idesc = dense_idesc(256, 256, BF, A_MN, B_K);
-      int it = 0, count = 0;
-      bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs, ++count) {
+  } else if (warp == 9) {   // ---- MMA issuer (the leader's): the warp loops, one lane issues ----
+    if (leader) {
+      const uint32_t idesc = dense_idesc(256, bn, BF, A_MN, B_K);
+      const uint32_t a_low = slab_low<A_MN>(smem_u32(ring)), b_low = slab_low<!B_K>(smem_u32(ring) + kOperand);
+      int s = 0, count = 0, used = 0;
+      uint32_t ph = 0, at = 0;   // at: the stage's offset in 16-byte units
+      bool go = true;
+      for (int t = pair; t < tiles && go; t += pairs, ++count) {
         const int slot = count & 1;
-        if (!wait_bounded(smem_u32(&sm.acc_empty[slot]), ((uint32_t)(count >> 1) & 1u) ^ 1u, abort_flag))
-          break;
+        go = __all_sync(kFull, wait_bounded(smem_u32(&sm.acc_empty[slot]),
+                                            ((uint32_t)(count >> 1) & 1u) ^ 1u, abort_flag, limit));
+        if (!go) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t d = tmem + (uint32_t)slot * 256u;
-        for (int kb = 0; kb < args.kbt; ++kb, ++it) {
-          const int s = it % kPairStages;
-          ok = wait_bounded(smem_u32(&sm.full[s]), (uint32_t)(it / kPairStages) & 1u, abort_flag);
-          if (!ok) break;
-          *(volatile int*)&sm.consumed = it + 1;
+        for (int kb = 0; kb < args.kbt; ++kb) {
+          go = __all_sync(kFull, wait_bounded(smem_u32(&sm.full[s]), ph, abort_flag, limit));
+          if (!go) break;
           asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-          const uint32_t a0 = smem_u32(sm.A[s]), b0 = smem_u32(sm.B[s]);
+          ++used;
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kSlab / 16; ++k)
-            mma_f16<2>(d, slab_desc<A_MN>(a0, k), slab_desc<!B_K>(b0, k), idesc,
-                       (kb > 0 || k > 0) ? 1u : 0u);
-          commit_pair(smem_u32(&sm.empty[s]));
+            for (int k = 0; k < kSlab / 16; ++k)
+              mma_f16<2>(d, slab_desc(a_low + at + k * slab_step<A_MN>),
+                         slab_desc(b_low + at + k * slab_step<!B_K>), idesc, (kb > 0 || k > 0) ? 1u : 0u);
+            commit_pair(smem_u32(&sm.empty[s]));
+          }
+          __syncwarp();
+          at += stage_bytes >> 4;
+          if (++s == S) { s = 0; at = 0; ph ^= 1u; }
         }
-        if (ok) commit_pair(smem_u32(&sm.acc_full[slot]));
+        if (go && elect_one()) commit_pair(smem_u32(&sm.acc_full[slot]));
+        __syncwarp();
       }
-      commit_pair(smem_u32(&sm.done));   // completes once every issued MMA has finished
+      if (lane == 0) sm.consumed = used;
+      if (elect_one()) commit_pair(smem_u32(&sm.done));   // completes once every issued MMA has finished
+      __syncwarp();
     }
-    __syncwarp();
   } else {   // ---- epilogue: eight warps, each 32 rows x half of the columns ----
     const int q = warp & 3, half = warp >> 2;
-    const uint32_t stage = smem_u32(sm.stage[warp]);
+    const uint32_t stage = smem_u32(blocks) + (uint32_t)warp * kStoreBlock;
     const uint32_t empty0 = map_to_rank(smem_u32(&sm.acc_empty[0]), 0);
     const uint32_t empty1 = map_to_rank(smem_u32(&sm.acc_empty[1]), 0);
+    const int blocks_of_warp = bn / 128;   // blocks of 64 columns (DENSE_LINEAR, DENSE_GRAD)
     int count = 0;
     for (int t = pair; t < tiles; t += pairs, ++count) {
       const TilePos p = tile_at(t, args.tm, tn_all);
@@ -489,7 +744,7 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
       const int slot = count & 1;
       // one verdict for the warp: the tensor-memory loads below need all its lanes
       if (!__all_sync(kFull, wait_bounded(smem_u32(&sm.acc_full[slot]), (uint32_t)(count >> 1) & 1u,
-                                          abort_flag)))
+                                          abort_flag, limit)))
         break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       const uint32_t acc = tmem + (uint32_t)slot * 256u + ((uint32_t)(q * 32) << 16);
@@ -500,14 +755,14 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
       };
       if constexpr (EPI == DENSE_LINEAR) {
 #pragma unroll 1
-        for (int blk = 0; blk < 2; ++blk) {
-          const int c = half * 128 + blk * 64, col = nt * 256 + c;
+        for (int blk = 0; blk < blocks_of_warp; ++blk) {
+          const int c = half * (bn / 2) + blk * 64, col = nt * bn + c;
           stage_wait(lane);
 #pragma unroll 1
           for (int part = 0; part < 2; ++part) {
             float v[32];
             tmem_ld32(v, acc + (uint32_t)(c + part * 32));
-            if (blk == 1 && part == 1) release();
+            if (blk == blocks_of_warp - 1 && part == 1) release();
             epi_linear<BF, 4>(v, args, row, col + part * 32);
             uint4 w[4];
 #pragma unroll
@@ -517,18 +772,23 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
           stage_store(stage, lane, &maps.o[mat], col, row0, args);
         }
       } else if constexpr (EPI == DENSE_GATED) {
-        // columns [0, 128) are g and [128, 256) are u of 128 hidden columns
-        const int c = half * 64, col = nt * 128 + c;
+        // accumulator columns [0, bn / 2) are g, the others u; 64 hidden columns a
+        // warp (with bn 128 there is only work for the first of a quarter's two)
+        const int c = half * 64, col = nt * (bn / 2) + c;
+        if (c >= bn / 2) {
+          release();
+          continue;
+        }
 #pragma unroll 1
         for (int out = 0; out < args.outs; ++out) {
           stage_wait(lane);
 #pragma unroll 1
           for (int part = 0; part < 2; ++part) {
             float v[32];
-            tmem_ld32(v, acc + (uint32_t)(c + part * 32 + (out == 2 ? 128 : 0)));
+            tmem_ld32(v, acc + (uint32_t)(c + part * 32 + (out == 2 ? bn / 2 : 0)));
             if (out == 0) {
               float u[32];
-              tmem_ld32(u, acc + (uint32_t)(128 + c + part * 32));
+              tmem_ld32(u, acc + (uint32_t)(bn / 2 + c + part * 32));
               if (args.outs == 1 && part == 1) release();
               epi_gated<32>(v, u, args.act);
             } else if (out == 2 && part == 1) {
@@ -543,8 +803,8 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
         }
       } else {
 #pragma unroll 1
-        for (int blk = 0; blk < 2; ++blk) {
-          const int c = half * 128 + blk * 64, col = nt * 256 + c;
+        for (int blk = 0; blk < blocks_of_warp; ++blk) {
+          const int c = half * (bn / 2) + blk * 64, col = nt * bn + c;
           uint4 w[3][2][4];
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
@@ -559,7 +819,7 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
             }
             float v[32];
             tmem_ld32(v, acc + (uint32_t)(c + part * 32));
-            if (blk == 1 && part == 1) release();
+            if (blk == blocks_of_warp - 1 && part == 1) release();
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               epi_grad8<BF>(&v[8 * j], gv[j], uv[j], args.act, w[0][part][j], w[1][part][j],
@@ -587,8 +847,8 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
   if (warp == 8 && lane == 0 && *abort_flag) {
     // after a give-up: the copies that were issued land before shared memory goes
     if (leader)
-      for (int it = *(volatile int*)&sm.consumed; it < issued; ++it)
-        wait_drain(smem_u32(&sm.full[it % kPairStages]), (uint32_t)(it / kPairStages) & 1u);
+      for (int it = sm.consumed; it < issued; ++it)
+        wait_drain(smem_u32(&sm.full[it % S]), (uint32_t)(it / S) & 1u);
     const long long t0 = clock64();
     while (clock64() - t0 < 40000) {
     }
@@ -601,63 +861,54 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
 }
 
 // ---------------------------------------------------------------------------
-// Split-K cluster kernel, one 128 x BN tile per cluster
+// Few tokens: 128 output columns x up to 256 tokens a tile, K split over a cluster
+//
+// A stage carries 16 KB of weight and only 128 bytes a token, and a block of
+// one token costs no more tensor work than one of sixteen.
 // ---------------------------------------------------------------------------
-constexpr int kSplitThreads = 256;
+constexpr int kFewThreads = 256;
+constexpr int kFewMaxStages = 12;
+constexpr int kFewCluster = 8;
 
-template <int BN>
-struct SplitCfg {
-  static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? 3 : 4;
-  static constexpr uint32_t kBBytes = BN * kSlab * 2;
-  static constexpr uint32_t kStageBytes = kOperand + kBBytes;
-};
-
-template <int BN>
-struct __align__(1024) SplitShared {
-  using C = SplitCfg<BN>;
-  uint8_t A[C::kStages][kOperand];
-  uint8_t B[C::kStages][C::kBBytes];
-  unsigned long long full[C::kStages];
-  unsigned long long empty[C::kStages];
+struct FewBars {
+  unsigned long long full[kFewMaxStages];
+  unsigned long long empty[kFewMaxStages];
   unsigned long long accum;
   uint32_t tmem_base;
   int abort_flag;
   int consumed;
 };
 
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
-  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c),
-               "f"(d)
-               : "memory");
-}
+struct FewShape {
+  int tn;        // tokens of a tile: a multiple of 16, at most 256
+  int stages;
+  int tmem;      // tensor-memory columns: a power of two >= max(tn, 32)
+  int join;      // bytes after the ring for the join, or 0: it takes the ring's place
+};
 
-template <bool BF>
-__device__ __forceinline__ void store8(uint16_t* o, int64_t at, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(o + at) = pack8<BF>(v);
-}
-
-template <bool B_K, int EPI, bool BF, int BN>
-__global__ void __launch_bounds__(kSplitThreads)
-dense_split_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__ DenseArgs args,
-                   int log2c) {
-  using C = SplitCfg<BN>;
-  constexpr int S = C::kStages;
+template <bool B_K, int EPI, bool BF>
+__global__ void __launch_bounds__(kFewThreads)
+dense_few_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__ DenseArgs args,
+                 const FewShape fs) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  SplitShared<BN>& sm = *reinterpret_cast<SplitShared<BN>*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t x_bytes = (uint32_t)fs.tn * 128u, stage_bytes = kOperand + x_bytes;   // 1024-multiples
+  const int S = fs.stages;
+  FewBars& sm = *reinterpret_cast<FewBars*>(ring + (size_t)S * stage_bytes + fs.join);
+  uint8_t* join = fs.join > 0 ? ring + (size_t)S * stage_bytes : ring;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)blockIdx.x;          // the cluster spans the grid's x
+  const int rank = (int)blockIdx.x, ranks = (int)gridDim.x;   // the cluster spans the grid's x
   const int mat = (int)blockIdx.y / args.tn, nt = (int)blockIdx.y - mat * args.tn;
-  const int m0 = (int)blockIdx.z * kTile;
-  constexpr int kOutCols = EPI == DENSE_GATED ? BN / 2 : BN;   // output columns of the tile
+  constexpr int kOutCols = EPI == DENSE_GATED ? 64 : 128;     // output columns of the tile
   const int n0 = nt * kOutCols;
-  // this CTA's part of the K stages
-  const int kb_lo = (int)(((int64_t)args.kbt * rank) >> log2c);
-  const int kb_hi = (int)(((int64_t)args.kbt * (rank + 1)) >> log2c);
-  const int steps = kb_hi - kb_lo;
+  const int t0 = (int)blockIdx.z * fs.tn;
+  const int kb_lo = (int)((int64_t)args.kbt * rank / ranks);
+  const int steps = (int)((int64_t)args.kbt * (rank + 1) / ranks) - kb_lo;
   volatile int* abort_flag = &sm.abort_flag;
   pdl_trigger();
 
+  if (warp == 2 && lane < 4) prefetch_map(lane < 2 ? &maps.a[lane] : &maps.b[lane - 2]);
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&sm.full[s]), 1);
@@ -672,206 +923,90 @@ dense_split_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sm.tmem_base)),
-                 "r"(BN)
+                 "r"(fs.tmem)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = sm.tmem_base;
+  // every CTA of the cluster runs once this barrier is passed (waited for
+  // before the first access to another CTA's shared memory)
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
+  const long long limit = wait_limit();
 
   int issued = 0;
-  if (warp == 0) {
-    if (lane == 0) {   // ---- TMA producer ----
-      for (int i = 0; i < steps; ++i) {
-        const int s = i % S, kb = kb_lo + i;
-        if (!wait_bounded(smem_u32(&sm.empty[s]), ((uint32_t)(i / S) & 1u) ^ 1u, abort_flag)) break;
-        const int seg = kb >= args.kb0 ? 1 : 0;
-        const int k = (kb - (seg ? args.kb0 : 0)) * kSlab;
-        const uint32_t fb = smem_u32(&sm.full[s]), b0 = smem_u32(sm.B[s]);
-        mbar_expect_tx(fb, C::kStageBytes);
-        tma_load_2d(smem_u32(sm.A[s]), &maps.a[seg], k, m0, fb);
-        if constexpr (EPI == DENSE_GATED) {
-#pragma unroll
-          for (int j = 0; j < BN / 64; ++j) {
-            constexpr int kHalf = BN / 128;   // 64-column blocks of each weight
-            tma_load_2d(b0 + j * kBlock, &maps.b[j / kHalf], n0 + (j % kHalf) * 64, k, fb);
-          }
-        } else if constexpr (B_K) {
-          tma_load_2d(b0, &maps.b[seg | mat], k, n0, fb);
-        } else {
-#pragma unroll
-          for (int j = 0; j < BN / 64; ++j)
-            tma_load_2d(b0 + j * kBlock, &maps.b[seg | mat], n0 + j * 64, k, fb);
-        }
-        ++issued;
+  if (warp == 0) {   // ---- TMA producer: the warp loops, one lane issues ----
+    int s = 0;
+    uint32_t ph = 1;
+    for (int i = 0; i < steps; ++i) {
+      if (!__all_sync(kFull, wait_bounded(smem_u32(&sm.empty[s]), ph, abort_flag, limit))) break;
+      const int kb = kb_lo + i, seg = kb >= args.kb0 ? 1 : 0;
+      const int k = (kb - (seg ? args.kb0 : 0)) * kSlab;
+      const uint32_t fb = smem_u32(&sm.full[s]), w0 = smem_u32(ring) + (uint32_t)s * stage_bytes;
+      if (elect_one()) {
+        mbar_expect_tx(fb, stage_bytes);
+        weight_boxes<B_K, EPI>(maps, args, mat, n0, kb, [&](const CUtensorMap* map, int c0, int c1, uint32_t at) {
+          tma_load_2d(w0 + at, map, c0, c1, fb);
+        });
+        tma_load_2d(w0 + kOperand, &maps.a[seg], k, t0, fb);
       }
+      __syncwarp();
+      ++issued;
+      if (++s == S) { s = 0; ph ^= 1u; }
     }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) {   // ---- MMA issuer ----
-      constexpr uint32_t idesc = dense_idesc(kTile, BN, BF, false, B_K);
-      for (int i = 0; i < steps; ++i) {
-        const int s = i % S;
-        if (!wait_bounded(smem_u32(&sm.full[s]), (uint32_t)(i / S) & 1u, abort_flag)) break;
-        *(volatile int*)&sm.consumed = i + 1;
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const uint32_t a0 = smem_u32(sm.A[s]), b0 = smem_u32(sm.B[s]);
+  } else if (warp == 1) {   // ---- MMA issuer: the warp loops, one lane issues ----
+    const uint32_t idesc = dense_idesc(kTile, fs.tn, BF, !B_K, true);
+    const uint32_t w_low = slab_low<!B_K>(smem_u32(ring)), x_low = slab_low<false>(smem_u32(ring) + kOperand);
+    int s = 0, used = 0;
+    uint32_t ph = 0, at = 0;   // at: the stage's offset in 16-byte units
+    for (int i = 0; i < steps; ++i) {
+      if (!__all_sync(kFull, wait_bounded(smem_u32(&sm.full[s]), ph, abort_flag, limit))) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      ++used;
+      if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < kSlab / 16; ++k)
-          mma_f16<1>(tmem, slab_desc<false>(a0, k), slab_desc<!B_K>(b0, k), idesc,
-                     (i > 0 || k > 0) ? 1u : 0u);
+          mma_f16<1>(tmem, slab_desc(w_low + at + k * slab_step<!B_K>),
+                     slab_desc(x_low + at + k * slab_step<false>), idesc, (i > 0 || k > 0) ? 1u : 0u);
         commit_one(smem_u32(&sm.empty[s]));
       }
-      commit_one(smem_u32(&sm.accum));   // completes once every issued MMA has finished
+      __syncwarp();
+      at += stage_bytes >> 4;
+      if (++s == S) { s = 0; at = 0; ph ^= 1u; }
     }
+    if (lane == 0) sm.consumed = used;
+    if (elect_one()) commit_one(smem_u32(&sm.accum));   // completes once every issued MMA has finished
     __syncwarp();
   }
 
   const bool acc_done = wait_drain(smem_u32(&sm.accum), 0u);
-  __syncwarp();
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const int valid = min(kTile, args.rows - m0);    // rows of this tile
-  const int q = warp & 3, half = warp >> 2;
-  const int row = m0 + q * 32 + lane;
-  const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16);
   // one verdict for the CTA: the tensor-memory loads below need whole warps
   const bool ok = __syncthreads_and(acc_done && !*abort_flag) != 0;
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const int valid = min(fs.tn, args.rows - t0);    // tokens of this tile
+  const int own = (valid + ranks - 1) / ranks;     // rank r joins tokens [r own, (r + 1) own)
 
-  if (log2c == 0) {
-    // the tile's sums are complete: straight from tensor memory to the outputs
-    if (ok && q * 32 < valid) {
-#pragma unroll 1
-      for (int cc = 0; cc < kOutCols / 2; cc += 32) {
-        const int c = half * (kOutCols / 2) + cc, col = n0 + c;
-        float v[32];
-        if constexpr (EPI == DENSE_LINEAR) {
-          tmem_ld32(v, acc + (uint32_t)c);
-          epi_linear<BF, 4>(v, args, row, col);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (row < args.rows && col + 8 * j < args.cols)
-              store8<BF>(args.o[mat], (int64_t)row * args.ldo + col + 8 * j,
-                         *reinterpret_cast<float(*)[8]>(&v[8 * j]));
-        } else if constexpr (EPI == DENSE_GATED) {
-          float u[32];
-          tmem_ld32(v, acc + (uint32_t)c);
-          tmem_ld32(u, acc + (uint32_t)(BN / 2 + c));
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (row < args.rows && col + 8 * j < args.cols) {
-              const int64_t at = (int64_t)row * args.ldo + col + 8 * j;
-              if (args.outs == 3) {
-                store8<BF>(args.o[1], at, *reinterpret_cast<float(*)[8]>(&v[8 * j]));
-                store8<BF>(args.o[2], at, *reinterpret_cast<float(*)[8]>(&u[8 * j]));
-              }
-            }
-          epi_gated<32>(v, u, args.act);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (row < args.rows && col + 8 * j < args.cols)
-              store8<BF>(args.o[0], (int64_t)row * args.ldo + col + 8 * j,
-                         *reinterpret_cast<float(*)[8]>(&v[8 * j]));
-        } else {
-          tmem_ld32(v, acc + (uint32_t)c);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (row < args.rows && col + 8 * j < args.cols) {
-              const int64_t at = (int64_t)row * args.ldo + col + 8 * j;
-              uint4 dg, du, h;
-              epi_grad8<BF>(&v[8 * j], ld16(args.g + at), ld16(args.u + at), args.act, dg, du, h);
-              *reinterpret_cast<uint4*>(args.o[0] + at) = dg;
-              *reinterpret_cast<uint4*>(args.o[1] + at) = du;
-              *reinterpret_cast<uint4*>(args.o[2] + at) = h;
-            }
-        }
-      }
-    }
-  } else {
-    // Join: rank r owns output columns [r W, (r + 1) W) of the tile.  Every
-    // CTA sends its sums of those columns to r's shared memory (the ring, free
-    // once every CTA's MMAs are done), and r adds them in rank order.
-    const int lw = (EPI == DENSE_GATED ? 31 - __clz(BN / 2) : 31 - __clz(BN)) - log2c;   // log2 W
-    const int W = 1 << lw;
-    const int pitch = EPI == DENSE_GATED ? 2 * W : W;      // floats of a row in the join buffer
-    const int swz = min(8, pitch / 4) - 1;
-    const uint32_t buf = smem_u32(sm.A[0]);
-    cluster_sync();
-    if (ok && q * 32 < valid) {
-#pragma unroll 1
-      for (int cc = 0; cc < BN / 2; cc += 32) {
-        const int c = half * (BN / 2) + cc;
-        float v[32];
-        tmem_ld32(v, acc + (uint32_t)c);
-        if (row < args.rows) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int cj = (EPI == DENSE_GATED ? c - half * (BN / 2) : c) + 4 * j;
-            const int owner = cj >> lw;
-            const int lc = (cj & (W - 1)) + (EPI == DENSE_GATED && half ? W : 0);
-            const int chunk = (lc >> 2) ^ (lane & swz);
-            const uint32_t at = buf + (uint32_t)(((rank * kTile + q * 32 + lane) * pitch + chunk * 4) * 4);
-            st_cluster_v4(map_to_rank(at, (uint32_t)owner), v[4 * j], v[4 * j + 1], v[4 * j + 2],
-                          v[4 * j + 3]);
-          }
-        }
-      }
-    }
-    cluster_sync();
-    if (ok) {
-      const int chunks = W >> 3;   // 8-column chunks of a row
-      const int ranks = 1 << log2c;
-      for (int i = tid; i < valid * chunks; i += kSplitThreads) {
-        const int r = i / chunks, ch = i - r * chunks;
-        const int col = n0 + rank * W + ch * 8;
-        if (col >= args.cols) continue;
-        auto gather = [&](float (&v)[8], int first) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = 0.f;
-          for (int src = 0; src < ranks; ++src) {
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              const int chunk = ((first >> 2) + hh) ^ (r & swz);
-              const float4 f = *reinterpret_cast<const float4*>(
-                  &sm.A[0][0] + (size_t)((src * kTile + r) * pitch + chunk * 4) * 4);
-              v[4 * hh] += f.x; v[4 * hh + 1] += f.y; v[4 * hh + 2] += f.z; v[4 * hh + 3] += f.w;
-            }
-          }
-        };
-        const int64_t at = (int64_t)(m0 + r) * args.ldo + col;
-        float v[8];
-        gather(v, ch * 8);
-        if constexpr (EPI == DENSE_LINEAR) {
-          epi_linear<BF, 1>(v, args, m0 + r, col);
-          store8<BF>(args.o[mat], at, v);
-        } else if constexpr (EPI == DENSE_GATED) {
-          float u[8];
-          gather(u, W + ch * 8);
-          if (args.outs == 3) {
-            store8<BF>(args.o[1], at, v);
-            store8<BF>(args.o[2], at, u);
-          }
-          epi_gated<8>(v, u, args.act);
-          store8<BF>(args.o[0], at, v);
-        } else {
-          uint4 dg, du, h;
-          epi_grad8<BF>(v, ld16(args.g + at), ld16(args.u + at), args.act, dg, du, h);
-          *reinterpret_cast<uint4*>(args.o[0] + at) = dg;
-          *reinterpret_cast<uint4*>(args.o[1] + at) = du;
-          *reinterpret_cast<uint4*>(args.o[2] + at) = h;
-        }
-      }
-    }
+  if (ranks > 1) {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (fs.join == 0) cluster_sync();   // the ring is free once every CTA's MMAs are done
   }
+  if (ok)
+    join_send(smem_u32(join), tmem, warp, lane, valid, own, rank, [](int j) { return (uint32_t)j; });
+  if (ranks > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (ok) join_finish<EPI, BF>(join, args, mat, n0, t0, valid, own, rank, ranks);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (tid == 0 && *abort_flag)
-    for (int i = *(volatile int*)&sm.consumed; i < issued; ++i)
+    for (int i = sm.consumed; i < issued; ++i)
       wait_drain(smem_u32(&sm.full[i % S]), (uint32_t)(i / S) & 1u);
   __syncthreads();
   if (warp == 0)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(BN)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(fs.tmem)
                  : "memory");
 }
 
@@ -892,83 +1027,92 @@ bool map16(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a product is run: the pair kernel, or the split kernel with tiles of bn
-// columns and 2^log2c CTAs along K.
+// How a product is run: by the pair kernel with tiles of bn accumulator columns,
+// or by the few-token kernel with tiles of tn tokens, `parts` CTAs along K and
+// per_sm CTAs resident on an SM.
 struct DensePlan {
   bool pair;
-  int bn, log2c;
+  int bn, tn, parts, per_sm;
 };
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
 DensePlan plan_dense(const DenseGemm& d, int kbt) {
-  if (d.a_mn) return {true, 256, 0};
-  const int shrink = d.epi == DENSE_GATED ? 2 : 1;   // accumulator columns per output column
-  const int64_t pair_tiles = (int64_t)ceil_div(d.rows, 256) * ceil_div(d.cols * shrink, 256) * d.mats;
-  if (pair_tiles > kNumSMs / 4 && d.rows > 128) return {true, 256, 0};
-  DensePlan best{true, 256, 0};
-  double best_cost = 1e30;
-  for (int bn : {128, 256}) {
-    for (int l = 0; l <= 3; ++l) {
-      if ((1 << l) > kbt) break;
-      const int64_t ctas = (int64_t)ceil_div(d.rows, kTile) * ceil_div(d.cols * shrink, bn) * d.mats << l;
-      const int slots = kNumSMs * (bn == 128 ? 2 : 1);
-      const double waves = (double)ceil_div(ctas, slots);
-      const double cost = waves * (((double)kbt / (1 << l)) * (bn + 128) + 2000.0) * (bn == 128 ? 2 : 1);
-      if (cost < best_cost) {
-        best_cost = cost;
-        best = {false, bn, l};
-      }
-    }
-  }
-  return best;
+  const int shrink = d.epi == DENSE_GATED ? 2 : 1;   // accumulator columns of an output column
+  if (d.a_mn || d.rows > 256) return {true, 256, 0, 0, 0};
+  const int tn = ceil_div(d.rows, 16) * 16, per_sm = tn <= 128 ? 2 : 1;
+  const int tiles = d.mats * ceil_div(d.cols * shrink, 128);
+  const int parts = std::max(1, std::min({kFewCluster, kbt, per_sm * kNumSMs / tiles}));
+  return {false, 0, tn, parts, per_sm};
 }
 
-template <bool A_MN, bool B_K, int EPI, bool BF>
-cudaError_t launch_pair_kernel(const DenseMaps& maps, const DenseArgs& args, cudaStream_t stream) {
-  auto fn = dense_pair_kernel<A_MN, B_K, EPI, BF>;
-  const size_t smem = sizeof(PairShared) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)args.tm * args.tn * args.mats;
-  const int pairs = (int)std::min<int64_t>(tiles, kNumSMs / 2);
-  e = launch_pdl(fn, dim3(2 * pairs), dim3(kPairThreads), smem, stream, maps, args);
-  return e != cudaSuccess ? e : cudaPeekAtLastError();
-}
-
-template <bool B_K, int EPI, bool BF, int BN>
-cudaError_t launch_split_bn(const DenseMaps& maps, const DenseArgs& args, int log2c,
-                            cudaStream_t stream) {
-  auto fn = dense_split_kernel<B_K, EPI, BF, BN>;
-  const size_t smem = sizeof(SplitShared<BN>) + 1024;
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+template <typename... P>
+cudaError_t launch_cluster(void (*fn)(DenseMaps, DenseArgs, P...), dim3 grid, int threads, int cluster,
+                           size_t smem, cudaStream_t stream, const DenseMaps& maps, const DenseArgs& args,
+                           P... shape) {
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerCta);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1u << log2c, (unsigned)(args.tn * args.mats), (unsigned)args.tm);
-  cfg.blockDim = dim3(kSplitThreads);
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 1u << log2c;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, fn, maps, args, log2c);
+  e = cudaLaunchKernelEx(&cfg, fn, maps, args, shape...);
   return e != cudaSuccess ? e : cudaPeekAtLastError();
+}
+
+template <bool A_MN, bool B_K, int EPI, bool BF>
+cudaError_t launch_pair_kernel(const DensePlan& p, const DenseMaps& maps, const DenseArgs& args,
+                               cudaStream_t stream) {
+  PairShape ps;
+  ps.bn = p.bn;
+  const int stage_bytes = (int)kOperand + p.bn * 64;
+  const int extra = 1024 + (int)sizeof(PairBars) + 8 * (int)kStoreBlock;
+  ps.stages = std::min(kPairMaxStages, (kSmemPerCta - extra) / stage_bytes);
+  const int64_t tiles = (int64_t)args.tm * args.tn * args.mats;
+  const int pairs = (int)std::min<int64_t>(tiles, kNumSMs / 2);
+  return launch_cluster<PairShape>(dense_pair_kernel<A_MN, B_K, EPI, BF>, dim3(2 * pairs), kPairThreads, 2,
+                                   (size_t)ps.stages * stage_bytes + extra, stream, maps, args, ps);
+}
+
+template <bool B_K, int EPI, bool BF>
+cudaError_t launch_few(const DensePlan& p, const DenseMaps& maps, const DenseArgs& args,
+                       cudaStream_t stream) {
+  FewShape fs;
+  fs.tn = p.tn;
+  fs.tmem = 32;
+  while (fs.tmem < p.tn) fs.tmem *= 2;
+  const int stage_bytes = (int)kOperand + p.tn * 128, extra = 1024 + (int)sizeof(FewBars);
+  // shared memory of a CTA: half of the SM's 228 KB (less 1 KB a CTA), or what one CTA may have
+  const int budget = (p.per_sm == 2 ? 113 * 1024 : kSmemPerCta) - extra;
+  // The join: tn tokens x 128 columns of float32, rounded up to whole ranks.
+  // Up to 64 tokens it has a place of its own, which saves the cluster barrier
+  // that says that every ring is free; above, it takes the ring's.
+  const int join = ceil_div(p.tn, p.parts) * p.parts * 512;
+  fs.join = p.tn <= 64 ? join : 0;
+  const int fit = std::min(kFewMaxStages, (budget - fs.join) / stage_bytes);
+  fs.stages = std::max({2, fs.join > 0 ? 0 : ceil_div(join, stage_bytes),
+                        std::min(fit, ceil_div(args.kbt, p.parts))});
+  const size_t smem = (size_t)fs.stages * stage_bytes + fs.join + extra;
+  return launch_cluster<FewShape>(dense_few_kernel<B_K, EPI, BF>,
+                                  dim3((unsigned)p.parts, (unsigned)(args.tn * args.mats), (unsigned)args.tm),
+                                  kFewThreads, p.parts, smem, stream, maps, args, fs);
 }
 
 template <bool A_MN, bool B_K, int EPI, bool BF>
 cudaError_t launch_as(const DensePlan& p, const DenseMaps& maps, const DenseArgs& args,
                       cudaStream_t stream) {
-  if (p.pair) return launch_pair_kernel<A_MN, B_K, EPI, BF>(maps, args, stream);
-  if constexpr (!A_MN) {
-    if (p.bn == 256) return launch_split_bn<B_K, EPI, BF, 256>(maps, args, p.log2c, stream);
-    return launch_split_bn<B_K, EPI, BF, 128>(maps, args, p.log2c, stream);
-  }
+  if (p.pair) return launch_pair_kernel<A_MN, B_K, EPI, BF>(p, maps, args, stream);
+  if constexpr (!A_MN) return launch_few<B_K, EPI, BF>(p, maps, args, stream);
   return cudaErrorInvalidValue;
 }
 
@@ -994,8 +1138,8 @@ cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream) {
   a.cols = (int)d.cols;
   a.kb0 = kb;
   a.kbt = kbt;
-  a.tm = ceil_div(d.rows, p.pair ? 256 : kTile);
-  a.tn = ceil_div(d.cols, dual ? p.bn / 2 : p.bn);
+  a.tm = ceil_div(d.rows, p.pair ? 256 : p.tn);
+  a.tn = ceil_div(d.cols, (p.pair ? p.bn : 128) / (dual ? 2 : 1));
   a.mats = d.mats;
   a.outs = dual ? (d.o[1] != nullptr ? 3 : 1) : 1;
   a.act = d.act;
@@ -1009,16 +1153,22 @@ cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream) {
   const int n_a = d.two_segments ? 2 : 1, n_b = (d.two_segments || d.mats == 2 || dual) ? 2 : 1;
   for (int i = 0; i < n_a; ++i)
     if (!(d.a_mn ? map16(&maps.a[i], d.a[i], d.rows, d.K, d.lda, kSlab)
-                 : map16(&maps.a[i], d.a[i], d.K, d.rows, d.lda, kTile)))
+                 : map16(&maps.a[i], d.a[i], d.K, d.rows, d.lda, p.pair ? kTile : p.tn)))
       return cudaErrorInvalidValue;
   for (int i = 0; i < n_b; ++i)
-    if (!(d.b_k ? map16(&maps.b[i], d.b[i], d.K, d.cols, d.ldb, p.pair ? 128 : p.bn)
+    if (!(d.b_k ? map16(&maps.b[i], d.b[i], d.K, d.cols, d.ldb, p.pair ? p.bn / 2 : kTile)
                 : map16(&maps.b[i], d.b[i], d.cols, d.K, d.ldb, kSlab)))
       return cudaErrorInvalidValue;
   if (p.pair)   // the pair kernel stores its outputs with TMA
     for (int i = 0; i < 3; ++i)
       if (d.o[i] != nullptr && !map16(&maps.o[i], d.o[i], d.cols, d.rows, d.ldo, 32))
         return cudaErrorInvalidValue;
+  // the kernels prefetch every map: the unused ones repeat the first
+  if (n_a < 2) maps.a[1] = maps.a[0];
+  if (n_b < 2) maps.b[1] = maps.b[0];
+  if (p.pair)
+    for (int i = 1; i < 3; ++i)
+      if (d.o[i] == nullptr) maps.o[i] = maps.o[0];
   return d.bf16 ? launch_typed<true>(d, p, maps, a, stream) : launch_typed<false>(d, p, maps, a, stream);
 }
 
