@@ -532,41 +532,51 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _elsewhere(dev, stream):
-    """None when ``dev`` is the current device and no other stream is asked
-    for; else the context to run in."""
-    if stream is None and dev.index is not None and dev.index == torch.cuda.current_device():
+def _elsewhere(X, stream):
+    """None when X is on the current device and no other stream is asked for;
+    else the context to run in."""
+    index = X.get_device()
+    if index < 0:
+        raise ValueError(f"tensors must be on a CUDA device, got {X.device}")
+    if stream is None and index == torch.cuda.current_device():
         return None
-    if dev.type != "cuda":
-        raise ValueError(f"tensors must be on a CUDA device, got {dev}")
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    if s.device != dev:
-        raise ValueError(f"stream is on {s.device}, the tensors on {dev}")
+    s = stream if stream is not None else torch.cuda.current_stream(index)
+    if s.device != X.device:
+        raise ValueError(f"stream is on {s.device}, the tensors on {X.device}")
     return torch.cuda.stream(s)
 
 
-def _matrix(t, name, like, shape, contiguous=False):
-    """Check a 2-D tensor of ``like``'s type and device; returns its row stride."""
-    if t is not like and (t.dtype != like.dtype or t.device != like.device):
-        raise TypeError(f"{name} must be {like.dtype} on {like.device}, got {t.dtype} on {t.device}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous:
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        return shape[1]
-    if shape[1] > 1 and t.stride(1) != 1:
+def _matrix(t, name, X, rows, cols, contiguous=False):
+    """Check a 2-D tensor of X's type and device; returns its row stride."""
+    if t.dtype is not X.dtype or t.get_device() != X.get_device():
+        raise TypeError(f"{name} must be {X.dtype} on {X.device}, got {t.dtype} on {t.device}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+    ld, step = t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    # a single row has no stride of its own: any that the library accepts
-    return t.stride(0) if shape[0] > 1 else -(-shape[1] // 8) * 8
+    if rows <= 1:   # a single row has no stride of its own: any that the library accepts
+        return -(-cols // 8) * 8
+    if contiguous and ld != cols:
+        raise ValueError(f"{name} must be contiguous")
+    return ld
 
 
-def _dense_type(X, name):
-    if X.dtype not in _DTYPES:
+def _block(X, name):
+    """(dtype code, tokens, features) of a block of tokens."""
+    dt = _DTYPES.get(X.dtype)
+    if dt is None:
         raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {X.dtype}")
     if X.dim() != 2:
         raise ValueError(f"{name} must be 2-D (tokens, features)")
-    return _DTYPES[X.dtype]
+    rows, cols = X.shape
+    return dt, rows, cols
+
+
+def _width(W, name):
+    if W.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    return W.shape[1]
 
 
 def linear_act(X, WT, bias=None, act: int = ACT_NONE, residual=None, Y=None, stream=None):
@@ -575,30 +585,29 @@ def linear_act(X, WT, bias=None, act: int = ACT_NONE, residual=None, Y=None, str
     X (rows, K), WT (K, N) contiguous, bias (N,), residual and Y (rows, N);
     X, residual and Y may have row strides (multiples of 8).  Y may be the
     residual.  N must be a multiple of 8."""
-    dt = _dense_type(X, "X")
-    ctx = _elsewhere(X.device, stream)
+    dt, rows, K = _block(X, "X")
+    ctx = _elsewhere(X, stream)
     if ctx is not None:
         with ctx:
             return linear_act(X, WT, bias, act, residual, Y)
-    rows, K = X.shape
-    if WT.dim() != 2:
-        raise ValueError("WT must be 2-D (K, N)")
-    N = WT.shape[1]
-    ldx = _matrix(X, "X", X, (rows, K))
-    _matrix(WT, "WT", X, (K, N), contiguous=True)
-    ldr = 0
+    N = _width(WT, "WT")
+    ldx = _matrix(X, "X", X, rows, K)
+    _matrix(WT, "WT", X, K, N, True)
+    ldr = ldy = N
+    b = r = None
     if bias is not None:
-        if bias.shape != (N,) or bias.dtype != X.dtype or bias.device != X.device or not bias.is_contiguous():
+        if bias.shape != (N,) or bias.dtype is not X.dtype or bias.device != X.device or not bias.is_contiguous():
             raise ValueError(f"bias must be a contiguous {X.dtype} vector of {N} entries on {X.device}")
+        b = bias.data_ptr()
     if residual is not None:
-        ldr = _matrix(residual, "residual", X, (rows, N))
+        ldr, r = _matrix(residual, "residual", X, rows, N), residual.data_ptr()
     if Y is None:
-        Y, ldy = X.new_empty((rows, N)), N
+        Y = X.new_empty((rows, N))
     else:
-        ldy = _matrix(Y, "Y", X, (rows, N))
+        ldy = _matrix(Y, "Y", X, rows, N)
     _check("linear_act", _lib.linear_act(
-        X.data_ptr(), rows, K, ldx, WT.data_ptr(), N, _ptr(bias), int(act), _ptr(residual), ldr,
-        Y.data_ptr(), ldy, dt, _raw_stream(X.device.index)))
+        X.data_ptr(), rows, K, ldx, WT.data_ptr(), N, b, act, r, ldr, Y.data_ptr(), ldy, dt,
+        _raw_stream(X.get_device())))
     return Y
 
 
@@ -610,35 +619,33 @@ def gated_mlp(X, WgT, WuT, WdT, act: int = ACT_SILU, residual=None, Y=None, h_ou
     (d_model, d_ff) and WdT (d_ff, d_model) contiguous.  h_out, g_out and u_out
     (rows, d_ff) receive the hidden block and the two projections, which
     gated_mlp_backward takes."""
-    dt = _dense_type(X, "X")
-    ctx = _elsewhere(X.device, stream)
+    dt, rows, m = _block(X, "X")
+    ctx = _elsewhere(X, stream)
     if ctx is not None:
         with ctx:
             return gated_mlp(X, WgT, WuT, WdT, act, residual, Y, h_out, g_out, u_out)
-    rows, m = X.shape
-    if WgT.dim() != 2:
-        raise ValueError("WgT must be 2-D (d_model, d_ff)")
-    f = WgT.shape[1]
-    ldx = _matrix(X, "X", X, (rows, m))
-    _matrix(WgT, "WgT", X, (m, f), contiguous=True)
-    _matrix(WuT, "WuT", X, (m, f), contiguous=True)
-    _matrix(WdT, "WdT", X, (f, m), contiguous=True)
-    ldr = _matrix(residual, "residual", X, (rows, m)) if residual is not None else 0
+    f = _width(WgT, "WgT")
+    ldx = _matrix(X, "X", X, rows, m)
+    _matrix(WgT, "WgT", X, m, f, True)
+    _matrix(WuT, "WuT", X, m, f, True)
+    _matrix(WdT, "WdT", X, f, m, True)
+    ldr = _matrix(residual, "residual", X, rows, m) if residual is not None else m
     for name, t in (("h_out", h_out), ("g_out", g_out), ("u_out", u_out)):
         if t is not None:
-            _matrix(t, name, X, (rows, f), contiguous=True)
+            _matrix(t, name, X, rows, f, True)
+    ldy = m
     if Y is None:
-        Y, ldy = X.new_empty((rows, m)), m
+        Y = X.new_empty((rows, m))
     else:
-        ldy = _matrix(Y, "Y", X, (rows, m))
+        ldy = _matrix(Y, "Y", X, rows, m)
     ws, n = None, 0
     if h_out is None:
         n = workspace_bytes(OP_GATED_TOKENS, m, f, rows)
         ws = X.new_empty(n, dtype=torch.uint8)
     _check("gated_mlp", _lib.gated_mlp(
-        X.data_ptr(), rows, ldx, WgT.data_ptr(), WuT.data_ptr(), WdT.data_ptr(), m, f, int(act),
+        X.data_ptr(), rows, ldx, WgT.data_ptr(), WuT.data_ptr(), WdT.data_ptr(), m, f, act,
         _ptr(residual), ldr, Y.data_ptr(), ldy, _ptr(h_out), _ptr(g_out), _ptr(u_out), dt,
-        _ptr(ws), n, _raw_stream(X.device.index)))
+        _ptr(ws), n, _raw_stream(X.get_device())))
     return Y
 
 
@@ -649,42 +656,41 @@ def gated_mlp_backward(dY, X, g, u, WgT, WuT, WdT, act: int = ACT_SILU, dX=None,
 
     want_x or want_weights False leaves those out (None in their place).  Given
     gradient tensors are written, not added to."""
-    dt = _dense_type(X, "X")
-    ctx = _elsewhere(X.device, stream)
+    dt, rows, m = _block(X, "X")
+    ctx = _elsewhere(X, stream)
     if ctx is not None:
         with ctx:
             return gated_mlp_backward(dY, X, g, u, WgT, WuT, WdT, act, dX, dWgT, dWuT, dWdT, want_x,
                                       want_weights)
-    rows, m = X.shape
-    if WgT.dim() != 2:
-        raise ValueError("WgT must be 2-D (d_model, d_ff)")
-    f = WgT.shape[1]
-    ldx = _matrix(X, "X", X, (rows, m))
-    lddy = _matrix(dY, "dY", X, (rows, m))
-    for name, t, shape in (("g", g, (rows, f)), ("u", u, (rows, f)), ("WgT", WgT, (m, f)),
-                           ("WuT", WuT, (m, f)), ("WdT", WdT, (f, m))):
-        _matrix(t, name, X, shape, contiguous=True)
-    lddx = 0
-    if want_x:
-        if dX is None:
-            dX = X.new_empty((rows, m))
-        lddx = _matrix(dX, "dX", X, (rows, m))
-    else:
+    f = _width(WgT, "WgT")
+    ldx = _matrix(X, "X", X, rows, m)
+    lddy = _matrix(dY, "dY", X, rows, m)
+    _matrix(g, "g", X, rows, f, True)
+    _matrix(u, "u", X, rows, f, True)
+    _matrix(WgT, "WgT", X, m, f, True)
+    _matrix(WuT, "WuT", X, m, f, True)
+    _matrix(WdT, "WdT", X, f, m, True)
+    lddx = m
+    if not want_x:
         dX = None
+    elif dX is None:
+        dX = X.new_empty((rows, m))
+    else:
+        lddx = _matrix(dX, "dX", X, rows, m)
     if want_weights:
-        dWgT = torch.empty_like(WgT) if dWgT is None else dWgT
-        dWuT = torch.empty_like(WuT) if dWuT is None else dWuT
-        dWdT = torch.empty_like(WdT) if dWdT is None else dWdT
-        for name, t, shape in (("dWgT", dWgT, (m, f)), ("dWuT", dWuT, (m, f)), ("dWdT", dWdT, (f, m))):
-            _matrix(t, name, X, shape, contiguous=True)
+        given = ((dWgT, "dWgT", m, f), (dWuT, "dWuT", m, f), (dWdT, "dWdT", f, m))
+        for t, name, r, c in given:
+            if t is not None:
+                _matrix(t, name, X, r, c, True)
+        dWgT, dWuT, dWdT = (X.new_empty((r, c)) if t is None else t for t, _, r, c in given)
     else:
         dWgT = dWuT = dWdT = None
     n = workspace_bytes(OP_GATED_BACKWARD, m, f, rows)
     ws = X.new_empty(n, dtype=torch.uint8)
     _check("gated_mlp_backward", _lib.gated_mlp_backward(
         dY.data_ptr(), lddy, X.data_ptr(), ldx, rows, g.data_ptr(), u.data_ptr(), WgT.data_ptr(),
-        WuT.data_ptr(), WdT.data_ptr(), m, f, int(act), _ptr(dX), lddx, _ptr(dWgT), _ptr(dWuT),
-        _ptr(dWdT), dt, ws.data_ptr(), n, _raw_stream(X.device.index)))
+        WuT.data_ptr(), WdT.data_ptr(), m, f, act, _ptr(dX), lddx, _ptr(dWgT), _ptr(dWuT),
+        _ptr(dWdT), dt, ws.data_ptr(), n, _raw_stream(X.get_device())))
     return dX, dWgT, dWuT, dWdT
 
 

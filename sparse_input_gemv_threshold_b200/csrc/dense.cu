@@ -19,6 +19,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "../../include/sig.h"
 
@@ -42,9 +43,11 @@ struct DenseArgs {
   int rows, cols;      // rows (tokens) and columns of one output
   int kb0, kbt;        // K stages of the first segment, of both
   int tm, tn;          // tiles down, and across one weight
+  int whole, items;    // pair kernel: tiles taken whole, and all items of the walk
   int mats;
   int outs;            // outputs to store (DENSE_GATED: 1, or 3 with g and u)
   int act;
+  bool plain;          // DENSE_LINEAR: no bias, activation or residual
   const uint16_t* bias;
   const uint16_t* residual;
   int64_t ldr;
@@ -110,8 +113,11 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
   return true;
 }
 
+// Hands an accumulator back: the tensor-memory loads are done and fenced, and no
+// other memory is passed on, so the arrive needs no release (whose wait for the
+// warp's earlier stores costs 15 us of 59 at 4096 x 16 x 22016, all epilogue).
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
 
@@ -183,9 +189,9 @@ __device__ __forceinline__ void commit_one(uint32_t bar) {
       : "memory");
 }
 
-// 32 accumulator columns of this warp's 32 rows (one row a lane).
-__device__ __forceinline__ void tmem_ld32(float (&v)[32], uint32_t addr) {
-  uint32_t r[32];
+// Start the load of 32 accumulator columns of this warp's 32 rows (one row a
+// lane); the values are there after tmem_wait32.
+__device__ __forceinline__ void tmem_start32(uint32_t (&r)[32], uint32_t addr) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -196,7 +202,22 @@ __device__ __forceinline__ void tmem_ld32(float (&v)[32], uint32_t addr) {
         "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Wait for the loads so far.  The registers pass through the wait, so that no
+// use of them can move above it.
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]),
+                 "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                 "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void as_floats(float (&v)[32], const uint32_t (&r)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
@@ -472,13 +493,14 @@ __device__ __forceinline__ void weight_boxes(const DenseMaps& maps, const DenseA
 template <bool BF, int G>
 __device__ __forceinline__ void epi_linear(float* v, const DenseArgs& a, int row, int col) {
   uint4 res[G];
-  const bool has_res = a.residual != nullptr && row < a.rows;
+  if (a.residual != nullptr) {
 #pragma unroll
-  for (int j = 0; j < G; ++j)
-    res[j] = has_res && col + 8 * j < a.cols
-                 // plain load: Y may be the residual buffer itself
-                 ? *reinterpret_cast<const uint4*>(a.residual + (int64_t)row * a.ldr + col + 8 * j)
-                 : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < G; ++j)
+      res[j] = row < a.rows && col + 8 * j < a.cols
+                   // plain load: Y may be the residual buffer itself
+                   ? *reinterpret_cast<const uint4*>(a.residual + (int64_t)row * a.ldr + col + 8 * j)
+                   : make_uint4(0, 0, 0, 0);
+  }
   if (a.bias != nullptr) {
 #pragma unroll
     for (int j = 0; j < G; ++j)
@@ -492,7 +514,8 @@ __device__ __forceinline__ void epi_linear(float* v, const DenseArgs& a, int row
   if (a.act != SIG_ACT_NONE)
     with_act(a.act, [&](auto A) {
 #pragma unroll
-      for (int i = 0; i < 8 * G; ++i) v[i] = act_value<decltype(A)::value>(v[i], act_share<decltype(A)::value>(v[i]));
+      for (int i = 0; i < 8 * G; ++i)
+        v[i] = act_value<decltype(A)::value>(v[i], act_share<decltype(A)::value>(v[i]));
     });
   if (a.residual != nullptr) {
 #pragma unroll
@@ -537,20 +560,28 @@ __device__ __forceinline__ void epi_grad8(const float* dh, const uint4& gv, cons
 }
 
 // ---------------------------------------------------------------------------
-// Persistent CTA pairs: tiles of 256 tokens x 128 or 256 accumulator columns
+// Persistent CTA pairs: tiles of 256 tokens x 256 (or 128) accumulator columns
+//
+// Tensor memory holds two accumulators of 256 columns, taken in turn, so the
+// epilogue of a tile runs beside the mainloop of the next; it hands an
+// accumulator back as soon as its last columns are in registers.  When the
+// tiles left after the last whole wave of CTA pairs are at most half a wave,
+// each is cut into two of 128 columns, so that the wave takes less time: a stage
+// of 128 columns takes 0.19 us against 0.275 us (256 x 8192 x 256), and
+// 512 x 4096 x 4096 19.2 against 25.3 us.
 // ---------------------------------------------------------------------------
 constexpr int kPairThreads = 320;                  // 8 epilogue warps, one loads, one issues MMAs
-constexpr int kPairMaxStages = 8;
+constexpr int kPairStages = 5;
 constexpr uint32_t kOperand = kTile * kSlab * 2;   // 16 KB: 128 rows (or columns) x 64 K
-constexpr uint32_t kStoreBlock = 32 * 128;         // per epilogue warp: 32 rows x 64 columns
+constexpr uint32_t kStoreBlock = 32 * 128;         // 32 rows x 64 columns; an epilogue warp has two
 constexpr int kGroupRows = 8;                      // row tiles walked together (L2 reuse of B)
-constexpr int kSmemPerCta = 227 * 1024;
+constexpr int kSmemPerCta = 227 * 1024, kSmemPerSm = 228 * 1024;   // a CTA costs 1 KB more than it asks for
 
 // After the ring (stage: 128 rows of A, then this CTA's half of the columns
 // of B) and the eight epilogue warps' store blocks.
 struct PairBars {
-  unsigned long long full[kPairMaxStages];         // used in the leader
-  unsigned long long empty[kPairMaxStages];
+  unsigned long long full[kPairStages];         // used in the leader
+  unsigned long long empty[kPairStages];
   unsigned long long acc_full[2], acc_empty[2];    // acc_empty used in the leader
   unsigned long long done;
   uint32_t tmem_base;
@@ -558,66 +589,77 @@ struct PairBars {
   int consumed;
 };
 
-struct PairShape {
-  int bn;        // accumulator columns of a tile: 128 or 256
-  int stages;
-};
-
+// Item t of the walk: a tile of 256 accumulator columns, or, from `whole` on,
+// one of the two halves of a tile.
 struct TilePos {
-  int m, n;
+  int m, mat, n;   // row tile, weight, accumulator column
+  int bn;          // 256 or 128
 };
 
-__device__ __forceinline__ TilePos tile_at(int t, int tm, int tn_all) {
-  const int per = kGroupRows * tn_all;
-  const int g0 = t / per * kGroupRows, r = t % per;
-  const int gs = min(kGroupRows, tm - g0);
-  return {g0 + r % gs, r / gs};
+__device__ __forceinline__ TilePos tile_at(int t, const DenseArgs& a) {
+  const int half = t < a.whole ? 0 : 1;
+  const int u = half ? a.whole + (t - a.whole) / 2 : t;
+  const int tn_all = a.tn * a.mats, per = kGroupRows * tn_all;
+  const int g0 = u / per * kGroupRows, r = u % per;
+  const int gs = min(kGroupRows, a.tm - g0);
+  const int n = r / gs, mat = n / a.tn;
+  return {g0 + r % gs, mat, (n - mat * a.tn) * 256 + (half ? (t - a.whole) % 2 * 128 : 0), half ? 128 : 256};
 }
 
-// Write 32 rows x 32 columns (16 packed words a lane) into a warp's staging
-// block at column 32 * part, in the 128-byte swizzled order of the store map.
-__device__ __forceinline__ void stage_words(uint32_t stage, int lane, int part, const uint4 (&p)[4]) {
+// Write 32 rows x 32 columns (64 bytes a lane) into a store block at column
+// 32 * part, in the 128-byte swizzled order of a store map 64 columns wide ...
+__device__ __forceinline__ void stage_words(uint32_t block, int lane, int part, const uint4 (&p)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t addr = stage + (uint32_t)lane * 128u + (uint32_t)(((part * 4 + j) ^ (lane & 7)) << 4);
+    const uint32_t addr = block + (uint32_t)lane * 128u + (uint32_t)(((part * 4 + j) ^ (lane & 7)) << 4);
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(p[j].x), "r"(p[j].y),
                  "r"(p[j].z), "r"(p[j].w)
                  : "memory");
   }
 }
 
-// The staging block is free once the stores before have read it.
+// ... or into a 2 KB block in the 64-byte swizzled order of a map 32 columns wide.
+__device__ __forceinline__ void stage_narrow(uint32_t block, int lane, const uint4 (&p)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t addr = block + (uint32_t)lane * 64u + (uint32_t)((j ^ ((lane >> 1) & 3)) << 4);
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(p[j].x), "r"(p[j].y),
+                 "r"(p[j].z), "r"(p[j].w)
+                 : "memory");
+  }
+}
+
+// A block is free once the stores from it have read it; `N` later ones may be on their way.
+template <int N>
 __device__ __forceinline__ void stage_wait(int lane) {
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
   __syncwarp();
 }
 
-__device__ __forceinline__ void stage_store(uint32_t stage, int lane, const CUtensorMap* map, int col,
+__device__ __forceinline__ void stage_store(uint32_t block, int lane, const CUtensorMap* map, int col,
                                             int row, const DenseArgs& a) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
   if (lane == 0) {
-    if (row < a.rows && col < a.cols) tma_store_2d(map, stage, col, row);   // the map clips the rest
+    if (row < a.rows && col < a.cols) tma_store_2d(map, block, col, row);   // the map clips the rest
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
 }
 
 template <bool A_MN, bool B_K, int EPI, bool BF>
 __global__ void __launch_bounds__(kPairThreads, 1)
-dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__ DenseArgs args,
-                  const PairShape ps) {
+dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__ DenseArgs args) {
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  const int S = ps.stages, bn = ps.bn;
-  const uint32_t stage_bytes = kOperand + (uint32_t)bn * 64u;
+  constexpr int S = kPairStages;
+  constexpr uint32_t stage_bytes = 2 * kOperand;   // 128 rows of A and up to 128 columns of B
   uint8_t* blocks = ring + (size_t)S * stage_bytes;
-  PairBars& sm = *reinterpret_cast<PairBars*>(blocks + 8 * kStoreBlock);
+  PairBars& sm = *reinterpret_cast<PairBars*>(blocks + 16 * kStoreBlock);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int tn_all = args.tn * args.mats, tiles = args.tm * tn_all;
   volatile int* abort_flag = &sm.abort_flag;
   pdl_trigger();
 
@@ -658,34 +700,34 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
     uint32_t ph = 1;
     bool go = true;
     const uint32_t full0 = map_to_rank(smem_u32(&sm.full[0]), 0);
-    for (int t = pair; t < tiles && go; t += pairs) {
-      const TilePos p = tile_at(t, args.tm, tn_all);
+    for (int t = pair; t < args.items && go; t += pairs) {
+      const TilePos p = tile_at(t, args);
       const int m0 = p.m * 256 + (int)rank * 128;
-      const int mat = p.n / args.tn, nt = p.n - mat * args.tn;
       // DENSE_GATED: CTA 0 brings the gate's columns, CTA 1 the up's
-      const int nb = EPI == DENSE_GATED ? nt * (bn / 2) : nt * bn + (int)rank * (bn / 2);
+      const int nb = EPI == DENSE_GATED ? p.n / 2 : p.n + (int)rank * (p.bn / 2);
       for (int kb = 0; kb < args.kbt; ++kb) {
         go = __all_sync(kFull, wait_bounded(smem_u32(&sm.empty[s]), ph, abort_flag, limit));
         if (!go) break;
         const int seg = kb >= args.kb0 ? 1 : 0;
         const int k = (kb - (seg ? args.kb0 : 0)) * kSlab;
         const CUtensorMap* ma = &maps.a[seg];
-        const CUtensorMap* mb = &maps.b[EPI == DENSE_GATED ? (int)rank : seg | mat];
+        const CUtensorMap* mb = &maps.b[EPI == DENSE_GATED ? (int)rank : seg | p.mat];
         const uint32_t fb = full0 + (uint32_t)s * 8u;
         const uint32_t a0 = smem_u32(ring) + (uint32_t)s * stage_bytes, b0 = a0 + kOperand;
         if (elect_one()) {
-          if (leader) mbar_expect_tx(smem_u32(&sm.full[s]), 2 * stage_bytes);
+          if (leader) mbar_expect_tx(smem_u32(&sm.full[s]), 2 * (kOperand + (uint32_t)p.bn * 64u));
           if constexpr (A_MN) {
             tma_load_2d_pair(a0, ma, m0, k, fb);
             tma_load_2d_pair(a0 + kBlock, ma, m0 + 64, k, fb);
           } else {
             tma_load_2d_pair(a0, ma, k, m0, fb);
           }
-          if constexpr (B_K) {
-            tma_load_2d_pair(b0, mb, k, nb, fb);
-          } else {
-            tma_load_2d_pair(b0, mb, nb, k, fb);
-            if (bn == 256) tma_load_2d_pair(b0 + kBlock, mb, nb + 64, k, fb);
+          // 64 columns a box
+          for (int j = 0; j < p.bn / 128; ++j) {
+            if constexpr (B_K)
+              tma_load_2d_pair(b0 + j * kBlock, mb, k, nb + j * 64, fb);
+            else
+              tma_load_2d_pair(b0 + j * kBlock, mb, nb + j * 64, k, fb);
           }
         }
         __syncwarp();
@@ -695,13 +737,13 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
     }
   } else if (warp == 9) {   // ---- MMA issuer (the leader's): the warp loops, one lane issues ----
     if (leader) {
-      const uint32_t idesc = dense_idesc(256, bn, BF, A_MN, B_K);
       const uint32_t a_low = slab_low<A_MN>(smem_u32(ring)), b_low = slab_low<!B_K>(smem_u32(ring) + kOperand);
       int s = 0, count = 0, used = 0;
       uint32_t ph = 0, at = 0;   // at: the stage's offset in 16-byte units
       bool go = true;
-      for (int t = pair; t < tiles && go; t += pairs, ++count) {
+      for (int t = pair; t < args.items && go; t += pairs, ++count) {
         const int slot = count & 1;
+        const uint32_t idesc = dense_idesc(256, t < args.whole ? 256 : 128, BF, A_MN, B_K);
         go = __all_sync(kFull, wait_bounded(smem_u32(&sm.acc_empty[slot]),
                                             ((uint32_t)(count >> 1) & 1u) ^ 1u, abort_flag, limit));
         if (!go) break;
@@ -718,13 +760,12 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
               mma_f16<2>(d, slab_desc(a_low + at + k * slab_step<A_MN>),
                          slab_desc(b_low + at + k * slab_step<!B_K>), idesc, (kb > 0 || k > 0) ? 1u : 0u);
             commit_pair(smem_u32(&sm.empty[s]));
+            if (kb == args.kbt - 1) commit_pair(smem_u32(&sm.acc_full[slot]));
           }
           __syncwarp();
           at += stage_bytes >> 4;
           if (++s == S) { s = 0; at = 0; ph ^= 1u; }
         }
-        if (go && elect_one()) commit_pair(smem_u32(&sm.acc_full[slot]));
-        __syncwarp();
       }
       if (lane == 0) sm.consumed = used;
       if (elect_one()) commit_pair(smem_u32(&sm.done));   // completes once every issued MMA has finished
@@ -732,16 +773,27 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
     }
   } else {   // ---- epilogue: eight warps, each 32 rows x half of the columns ----
     const int q = warp & 3, half = warp >> 2;
-    const uint32_t stage = smem_u32(blocks) + (uint32_t)warp * kStoreBlock;
+    const uint32_t store = smem_u32(blocks) + (uint32_t)warp * 2 * kStoreBlock;
     const uint32_t empty0 = map_to_rank(smem_u32(&sm.acc_empty[0]), 0);
     const uint32_t empty1 = map_to_rank(smem_u32(&sm.acc_empty[1]), 0);
-    const int blocks_of_warp = bn / 128;   // blocks of 64 columns (DENSE_LINEAR, DENSE_GRAD)
     int count = 0;
-    for (int t = pair; t < tiles; t += pairs, ++count) {
-      const TilePos p = tile_at(t, args.tm, tn_all);
+    uint32_t next = 0;   // the store block written next: 0 or kStoreBlock
+    for (int t = pair; t < args.items; t += pairs, ++count) {
+      const TilePos p = tile_at(t, args);
       const int row0 = p.m * 256 + (int)rank * 128 + q * 32, row = row0 + lane;
-      const int mat = p.n / args.tn, nt = p.n - mat * args.tn;
+      const int blocks_of_warp = p.bn / 128;   // blocks of 64 columns (DENSE_LINEAR, DENSE_GRAD)
       const int slot = count & 1;
+      uint4 gn[4], un[4];   // DENSE_GRAD: g and u of this row's next 32 columns
+      auto fetch_gu = [&](int r, int col) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool in = r < args.rows && col + 8 * j < args.cols;
+          const int64_t at = (int64_t)r * args.cols + col + 8 * j;
+          gn[j] = in ? ld16(args.g + at) : make_uint4(0, 0, 0, 0);
+          un[j] = in ? ld16(args.u + at) : make_uint4(0, 0, 0, 0);
+        }
+      };
+      if constexpr (EPI == DENSE_GRAD) fetch_gu(row, p.n + half * (p.bn / 2));
       // one verdict for the warp: the tensor-memory loads below need all its lanes
       if (!__all_sync(kFull, wait_bounded(smem_u32(&sm.acc_full[slot]), (uint32_t)(count >> 1) & 1u,
                                           abort_flag, limit)))
@@ -756,81 +808,97 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
       if constexpr (EPI == DENSE_LINEAR) {
 #pragma unroll 1
         for (int blk = 0; blk < blocks_of_warp; ++blk) {
-          const int c = half * (bn / 2) + blk * 64, col = nt * bn + c;
-          stage_wait(lane);
-#pragma unroll 1
+          const int c = half * (p.bn / 2) + blk * 64, col = p.n + c;
+#pragma unroll
           for (int part = 0; part < 2; ++part) {
-            float v[32];
-            tmem_ld32(v, acc + (uint32_t)(c + part * 32));
+            uint32_t r[32];
+            tmem_start32(r, acc + (uint32_t)(c + part * 32));
+            tmem_wait32(r);
             if (blk == blocks_of_warp - 1 && part == 1) release();
-            epi_linear<BF, 4>(v, args, row, col + part * 32);
+            float v[32];
+            as_floats(v, r);
+            if (!args.plain) epi_linear<BF, 4>(v, args, row, col + part * 32);
             uint4 w[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[j] = pack8<BF>(*reinterpret_cast<float(*)[8]>(&v[8 * j]));
-            stage_words(stage, lane, part, w);
+            if (part == 0) stage_wait<1>(lane);
+            stage_words(store + next, lane, part, w);
           }
-          stage_store(stage, lane, &maps.o[mat], col, row0, args);
+          stage_store(store + next, lane, &maps.o[p.mat], col, row0, args);
+          next ^= kStoreBlock;
         }
       } else if constexpr (EPI == DENSE_GATED) {
-        // accumulator columns [0, bn / 2) are g, the others u; 64 hidden columns a
+        // accumulator columns [0, p.bn / 2) are g, the others u; 64 hidden columns a
         // warp (with bn 128 there is only work for the first of a quarter's two)
-        const int c = half * 64, col = nt * (bn / 2) + c;
-        if (c >= bn / 2) {
+        const int c = half * 64, col = p.n / 2 + c;
+        if (c >= p.bn / 2) {
           release();
           continue;
         }
-#pragma unroll 1
-        for (int out = 0; out < args.outs; ++out) {
-          stage_wait(lane);
-#pragma unroll 1
-          for (int part = 0; part < 2; ++part) {
-            float v[32];
-            tmem_ld32(v, acc + (uint32_t)(c + part * 32 + (out == 2 ? bn / 2 : 0)));
-            if (out == 0) {
-              float u[32];
-              tmem_ld32(u, acc + (uint32_t)(bn / 2 + c + part * 32));
-              if (args.outs == 1 && part == 1) release();
-              epi_gated<32>(v, u, args.act);
-            } else if (out == 2 && part == 1) {
-              release();
-            }
-            uint4 w[4];
+        uint4 w[3][2][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = pack8<BF>(*reinterpret_cast<float(*)[8]>(&v[8 * j]));
-            stage_words(stage, lane, part, w);
-          }
-          stage_store(stage, lane, &maps.o[out], col, row0, args);
-        }
-      } else {
-#pragma unroll 1
-        for (int blk = 0; blk < blocks_of_warp; ++blk) {
-          const int c = half * (bn / 2) + blk * 64, col = nt * bn + c;
-          uint4 w[3][2][4];
-#pragma unroll
-          for (int part = 0; part < 2; ++part) {
-            uint4 gv[4], uv[4];
+        for (int part = 0; part < 2; ++part) {
+          uint32_t rg[32], ru[32];
+          tmem_start32(rg, acc + (uint32_t)(c + part * 32));
+          tmem_start32(ru, acc + (uint32_t)(p.bn / 2 + c + part * 32));
+          tmem_wait32(rg);
+          tmem_wait32(ru);
+          if (part == 1) release();
+          float g[32], u[32];
+          as_floats(g, rg);
+          as_floats(u, ru);
+          if (args.outs == 3) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const int cj = col + part * 32 + 8 * j;
-              const bool in = row < args.rows && cj < args.cols;
-              const int64_t at = (int64_t)row * args.cols + cj;
-              gv[j] = in ? ld16(args.g + at) : make_uint4(0, 0, 0, 0);
-              uv[j] = in ? ld16(args.u + at) : make_uint4(0, 0, 0, 0);
+              w[1][part][j] = pack8<BF>(*reinterpret_cast<float(*)[8]>(&g[8 * j]));
+              w[2][part][j] = pack8<BF>(*reinterpret_cast<float(*)[8]>(&u[8 * j]));
             }
-            float v[32];
-            tmem_ld32(v, acc + (uint32_t)(c + part * 32));
-            if (blk == blocks_of_warp - 1 && part == 1) release();
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              epi_grad8<BF>(&v[8 * j], gv[j], uv[j], args.act, w[0][part][j], w[1][part][j],
-                            w[2][part][j]);
           }
+          epi_gated<32>(g, u, args.act);
 #pragma unroll
-          for (int out = 0; out < 3; ++out) {
-            stage_wait(lane);
-            stage_words(stage, lane, 0, w[out][0]);
-            stage_words(stage, lane, 1, w[out][1]);
-            stage_store(stage, lane, &maps.o[out], col, row0, args);
+          for (int j = 0; j < 4; ++j) w[0][part][j] = pack8<BF>(*reinterpret_cast<float(*)[8]>(&g[8 * j]));
+        }
+#pragma unroll
+        for (int out = 0; out < 3; ++out) {
+          if (out >= args.outs) break;
+          stage_wait<1>(lane);
+          stage_words(store + next, lane, 0, w[out][0]);
+          stage_words(store + next, lane, 1, w[out][1]);
+          stage_store(store + next, lane, &maps.o[out], col, row0, args);
+          next ^= kStoreBlock;
+        }
+      } else {
+        // 32 columns at a time; g and u of the next 32 are on their way meanwhile,
+        // those of the first since before the accumulator was complete
+#pragma unroll 1
+        for (int i = 0; i < 2 * blocks_of_warp; ++i) {
+          const int c = half * (p.bn / 2) + i * 32, col = p.n + c;
+          uint4 gv[4], uv[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            gv[j] = gn[j];
+            uv[j] = un[j];
+          }
+          uint32_t r[32];
+          tmem_start32(r, acc + (uint32_t)c);
+          if (i < 2 * blocks_of_warp - 1) fetch_gu(row, col + 32);
+          tmem_wait32(r);
+          if (i == 2 * blocks_of_warp - 1) release();
+          float v[32];
+          as_floats(v, r);
+          uint4 w[3][4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            epi_grad8<BF>(&v[8 * j], gv[j], uv[j], args.act, w[0][j], w[1][j], w[2][j]);
+          stage_wait<0>(lane);
+#pragma unroll
+          for (int out = 0; out < 3; ++out) stage_narrow(store + out * 2048u, lane, w[out]);
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) {
+            if (row0 < args.rows && col < args.cols)
+              for (int out = 0; out < 3; ++out) tma_store_2d(&maps.o[out], store + out * 2048u, col, row0);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         }
       }
@@ -1014,43 +1082,98 @@ dense_few_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__
 // Host side
 // ---------------------------------------------------------------------------
 // 2-D map over 16-bit values: `inner` contiguous, `outer` rows `pitch` apart,
-// box 64 x `box` rows, 128-byte swizzle, zeros outside.
-bool map16(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t pitch, int box) {
+// box `width` (64, or 32) x `box` rows, swizzled by the box's row length of 128
+// (or 64) bytes, zeros outside.
+bool map16(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int64_t pitch, int box,
+           int width = 64) {
   auto enc = get_encode();
   if (enc == nullptr) return false;
   cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)outer};
   cuuint64_t strides[1] = {(cuuint64_t)pitch * 2};
-  cuuint32_t boxes[2] = {64, (cuuint32_t)box};
+  cuuint32_t boxes[2] = {(cuuint32_t)width, (cuuint32_t)box};
   cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, boxes,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             width == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a product is run: by the pair kernel with tiles of bn accumulator columns,
-// or by the few-token kernel with tiles of tn tokens, `parts` CTAs along K and
-// per_sm CTAs resident on an SM.
+// How a product is run: by the pair kernel, or by the few-token kernel with
+// tiles of tn tokens, `parts` CTAs along K and per_sm CTAs resident on an SM.
 struct DensePlan {
   bool pair;
-  int bn, tn, parts, per_sm;
+  int tn, parts, per_sm;
 };
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
+// Which kernel, and how a few-token launch is split.
+//
+// Up to 64 tokens the launch is bound by reading the weight and two CTAs fit an
+// SM.  K is split until there are 128 CTAs, and on while each keeps 16
+// stages and the clusters run at once: measured on B200 with 16 tokens, 4096 -> 4096 9.1 us with 4 parts
+// against 10.0 with 8 and 9.6 with 3; 11008 -> 4096 17.9 with 8 against 18.8
+// with 4; 4096 -> 11008 17.7 with 3 against 20.3 with 1.
+// From 65 to 1024 tokens both kernels are in play, bound by what a stage takes to
+// arrive (about 110 KB/us an SM): the few-token kernel with a few blocks of
+// tokens and K split over the SMs, or the pair kernel with its whole and half
+// tiles.  The estimates below (in us; the constants are those of the measured
+// stages, joins and launches) pick the faster one at 192 tokens: 4096 -> 4096
+// few 15.0 against 19.5 us, 4096 -> 11008 pair 26.6 against 29.8,
+// 1024 -> 2816 pair 8.7 against 8.8.  Beyond 1024 tokens the pair kernel fills
+// the GPU.
+// Clusters of 1 .. 8 CTAs are placed within a GPC, so fewer of the larger ones
+// fit at once: what cudaOccupancyMaxActiveClusters gives for the few-token
+// kernel's shared memory with one and with two CTAs on an SM.
+constexpr int kClusters1[kFewCluster + 1] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
+constexpr int kClusters2[kFewCluster + 1] = {0, 296, 148, 93, 71, 56, 45, 37, 33};
+
 DensePlan plan_dense(const DenseGemm& d, int kbt) {
+  const DensePlan pair = {true, 0, 0, 0};
+  if (d.a_mn || d.rows > 1024) return pair;
   const int shrink = d.epi == DENSE_GATED ? 2 : 1;   // accumulator columns of an output column
-  if (d.a_mn || d.rows > 256) return {true, 256, 0, 0, 0};
-  const int tn = ceil_div(d.rows, 16) * 16, per_sm = tn <= 128 ? 2 : 1;
-  const int tiles = d.mats * ceil_div(d.cols * shrink, 128);
-  const int parts = std::max(1, std::min({kFewCluster, kbt, per_sm * kNumSMs / tiles}));
-  return {false, 0, tn, parts, per_sm};
+  const int cols = d.mats * ceil_div(d.cols * shrink, 128);
+  if (d.rows <= 64) {
+    int parts = std::min({kFewCluster, kbt, std::max({1, kbt / 16, 128 / cols})});
+    while (parts > 1 && cols > kClusters2[parts]) --parts;
+    return {false, ceil_div(d.rows, 16) * 16, parts, 2};
+  }
+  const int tiles = ceil_div(d.rows, 256) * d.mats * ceil_div(d.cols * shrink, 256);
+  const int waves = tiles / (kNumSMs / 2), left = tiles % (kNumSMs / 2);
+  double best = 4.5 + kbt * (0.36 * waves + (left == 0 ? 0.0 : left <= kNumSMs / 4 ? 0.22 : 0.33));
+  DensePlan plan = pair;
+  for (int blocks = ceil_div(d.rows, 256); blocks <= ceil_div(d.rows, 128); ++blocks) {
+    const int tn = ceil_div(ceil_div(d.rows, blocks), 16) * 16, few = blocks * cols;
+    for (int parts = 1; parts <= std::min(kFewCluster, kbt); ++parts) {
+      const double stage = (16.0 + tn / 8.0) / 110.0, join = tn * 0.5 * (parts - 1) / parts / 20.0;
+      const double t = ceil_div(few, kClusters1[parts]) * (5.0 + ceil_div(kbt, parts) * stage) + join;
+      if (t < best) {
+        best = t;
+        plan = {false, tn, parts, 1};
+      }
+    }
+  }
+  return plan;
 }
 
-template <typename... P>
-cudaError_t launch_cluster(void (*fn)(DenseMaps, DenseArgs, P...), dim3 grid, int threads, int cluster,
-                           size_t smem, cudaStream_t stream, const DenseMaps& maps, const DenseArgs& args,
-                           P... shape) {
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerCta);
+// `FN` may use all the shared memory of a CTA: asked for once per device.
+template <auto FN>
+cudaError_t allow_shared() {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(FN, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerCta);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
+template <auto FN, typename... P>
+cudaError_t launch_cluster(dim3 grid, int threads, int cluster, size_t smem, cudaStream_t stream,
+                           const DenseMaps& maps, const DenseArgs& args, P... shape) {
+  cudaError_t e = allow_shared<FN>();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
@@ -1066,22 +1189,18 @@ cudaError_t launch_cluster(void (*fn)(DenseMaps, DenseArgs, P...), dim3 grid, in
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, fn, maps, args, shape...);
+  e = cudaLaunchKernelEx(&cfg, FN, maps, args, shape...);
   return e != cudaSuccess ? e : cudaPeekAtLastError();
 }
 
 template <bool A_MN, bool B_K, int EPI, bool BF>
-cudaError_t launch_pair_kernel(const DensePlan& p, const DenseMaps& maps, const DenseArgs& args,
-                               cudaStream_t stream) {
-  PairShape ps;
-  ps.bn = p.bn;
-  const int stage_bytes = (int)kOperand + p.bn * 64;
-  const int extra = 1024 + (int)sizeof(PairBars) + 8 * (int)kStoreBlock;
-  ps.stages = std::min(kPairMaxStages, (kSmemPerCta - extra) / stage_bytes);
-  const int64_t tiles = (int64_t)args.tm * args.tn * args.mats;
-  const int pairs = (int)std::min<int64_t>(tiles, kNumSMs / 2);
-  return launch_cluster<PairShape>(dense_pair_kernel<A_MN, B_K, EPI, BF>, dim3(2 * pairs), kPairThreads, 2,
-                                   (size_t)ps.stages * stage_bytes + extra, stream, maps, args, ps);
+cudaError_t launch_pair_kernel(const DenseMaps& maps, const DenseArgs& args, cudaStream_t stream) {
+  constexpr int kStageBytes = 2 * (int)kOperand;
+  constexpr int kSmem = kPairStages * kStageBytes + 16 * (int)kStoreBlock + (int)sizeof(PairBars) + 1024;
+  static_assert(kSmem <= kSmemPerCta, "ring, store blocks and barriers fit an SM");
+  const int pairs = std::min(args.items, kNumSMs / 2);
+  return launch_cluster<&dense_pair_kernel<A_MN, B_K, EPI, BF>>(dim3(2 * pairs), kPairThreads, 2, kSmem, stream,
+                                                                maps, args);
 }
 
 template <bool B_K, int EPI, bool BF>
@@ -1093,7 +1212,7 @@ cudaError_t launch_few(const DensePlan& p, const DenseMaps& maps, const DenseArg
   while (fs.tmem < p.tn) fs.tmem *= 2;
   const int stage_bytes = (int)kOperand + p.tn * 128, extra = 1024 + (int)sizeof(FewBars);
   // shared memory of a CTA: half of the SM's 228 KB (less 1 KB a CTA), or what one CTA may have
-  const int budget = (p.per_sm == 2 ? 113 * 1024 : kSmemPerCta) - extra;
+  const int budget = (p.per_sm == 2 ? kSmemPerSm / 2 - 1024 : kSmemPerCta) - extra;
   // The join: tn tokens x 128 columns of float32, rounded up to whole ranks.
   // Up to 64 tokens it has a place of its own, which saves the cluster barrier
   // that says that every ring is free; above, it takes the ring's.
@@ -1103,15 +1222,15 @@ cudaError_t launch_few(const DensePlan& p, const DenseMaps& maps, const DenseArg
   fs.stages = std::max({2, fs.join > 0 ? 0 : ceil_div(join, stage_bytes),
                         std::min(fit, ceil_div(args.kbt, p.parts))});
   const size_t smem = (size_t)fs.stages * stage_bytes + fs.join + extra;
-  return launch_cluster<FewShape>(dense_few_kernel<B_K, EPI, BF>,
-                                  dim3((unsigned)p.parts, (unsigned)(args.tn * args.mats), (unsigned)args.tm),
-                                  kFewThreads, p.parts, smem, stream, maps, args, fs);
+  return launch_cluster<&dense_few_kernel<B_K, EPI, BF>>(
+      dim3((unsigned)p.parts, (unsigned)(args.tn * args.mats), (unsigned)args.tm), kFewThreads, p.parts, smem,
+      stream, maps, args, fs);
 }
 
 template <bool A_MN, bool B_K, int EPI, bool BF>
 cudaError_t launch_as(const DensePlan& p, const DenseMaps& maps, const DenseArgs& args,
                       cudaStream_t stream) {
-  if (p.pair) return launch_pair_kernel<A_MN, B_K, EPI, BF>(p, maps, args, stream);
+  if (p.pair) return launch_pair_kernel<A_MN, B_K, EPI, BF>(maps, args, stream);
   if constexpr (!A_MN) return launch_few<B_K, EPI, BF>(p, maps, args, stream);
   return cudaErrorInvalidValue;
 }
@@ -1139,10 +1258,17 @@ cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream) {
   a.kb0 = kb;
   a.kbt = kbt;
   a.tm = ceil_div(d.rows, p.pair ? 256 : p.tn);
-  a.tn = ceil_div(d.cols, (p.pair ? p.bn : 128) / (dual ? 2 : 1));
+  a.tn = ceil_div(d.cols, (p.pair ? 256 : 128) / (dual ? 2 : 1));
   a.mats = d.mats;
+  if (p.pair) {
+    const int tiles = a.tm * a.tn * a.mats, left = tiles % (kNumSMs / 2);
+    const bool cut = left <= kNumSMs / 4;   // a remainder of at most half a wave is cut in two
+    a.whole = cut ? tiles - left : tiles;
+    a.items = cut ? tiles + left : tiles;
+  }
   a.outs = dual ? (d.o[1] != nullptr ? 3 : 1) : 1;
   a.act = d.act;
+  a.plain = d.bias == nullptr && d.act == SIG_ACT_NONE && d.residual == nullptr;
   a.bias = d.bias;
   a.residual = d.residual;
   a.ldr = d.ldr;
@@ -1156,12 +1282,12 @@ cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream) {
                  : map16(&maps.a[i], d.a[i], d.K, d.rows, d.lda, p.pair ? kTile : p.tn)))
       return cudaErrorInvalidValue;
   for (int i = 0; i < n_b; ++i)
-    if (!(d.b_k ? map16(&maps.b[i], d.b[i], d.K, d.cols, d.ldb, p.pair ? p.bn / 2 : kTile)
+    if (!(d.b_k ? map16(&maps.b[i], d.b[i], d.K, d.cols, d.ldb, p.pair ? 64 : kTile)
                 : map16(&maps.b[i], d.b[i], d.cols, d.K, d.ldb, kSlab)))
       return cudaErrorInvalidValue;
   if (p.pair)   // the pair kernel stores its outputs with TMA
     for (int i = 0; i < 3; ++i)
-      if (d.o[i] != nullptr && !map16(&maps.o[i], d.o[i], d.cols, d.rows, d.ldo, 32))
+      if (d.o[i] != nullptr && !map16(&maps.o[i], d.o[i], d.cols, d.rows, d.ldo, 32, d.epi == DENSE_GRAD ? 32 : 64))
         return cudaErrorInvalidValue;
   // the kernels prefetch every map: the unused ones repeat the first
   if (n_a < 2) maps.a[1] = maps.a[0];
