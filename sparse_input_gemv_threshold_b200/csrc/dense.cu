@@ -36,7 +36,7 @@ constexpr int kSlab = 64;       // K of one stage: a 128-byte swizzle row of 16-
 constexpr uint32_t kBlock = kSlab * 128;   // 64 rows of 128 bytes
 
 struct DenseMaps {
-  CUtensorMap a[2], b[2], o[3];
+  CUtensorMap a[2], b[2], o[3], r[2];   // r: the residual, or g and u
 };
 
 struct DenseArgs {
@@ -262,9 +262,29 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 }
 
 constexpr float kInvSqrt2 = 0.70710678118654752f;
+constexpr float kErfP = 0.3275911f;   // Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26
+constexpr float kErfA[5] = {0.254829592f, -0.284496736f, 1.421413741f, -1.453152027f, 1.061405429f};
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kGeluC = 0.79788456080286536f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
+
+// 1 / (1 + exp(-v)) with the hardware's exponential and reciprocal: a relative
+// error of about (3 + 1.2 |v|) 2^-23, and 0 where exp(-v) passes 2^126 (the IEEE
+// division took 16 us of 42 at 2048 x 1024 x 2816 with SiLU and its slope).
+__device__ __forceinline__ float logistic(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+
+// exp(-z^2 / 2)
+__device__ __forceinline__ float bell(float z) { return __expf(-0.5f * z * z); }
+
+// The normal distribution function, from Abramowitz and Stegun's erfc(x) =
+// t (a1 + t (a2 + ..)) exp(-x^2), t = 1 / (1 + p x), good to 1.5e-7 for x >= 0.
+// Its exponential is the one that the slope of GELU needs too.
+__device__ __forceinline__ float normal_cdf(float z) {
+  const float t = __fdividef(1.f, fmaf(kErfP * kInvSqrt2, fabsf(z), 1.f));
+  const float poly = fmaf(t, fmaf(t, fmaf(t, fmaf(t, kErfA[4], kErfA[3]), kErfA[2]), kErfA[1]), kErfA[0]);
+  const float tail = 0.5f * t * poly * bell(z);
+  return z >= 0.f ? 1.f - tail : tail;
+}
 
 // act(z) = z p(z); p is the share that passes (1, [z > 0], the logistic
 // function, the normal distribution function, or the logistic of the tanh
@@ -272,10 +292,10 @@ constexpr float kGeluA = 0.044715f;
 template <int ACT>
 __device__ __forceinline__ float act_share(float z) {
   if constexpr (ACT == SIG_ACT_RELU) return z > 0.f ? 1.f : 0.f;
-  if constexpr (ACT == SIG_ACT_SILU) return 1.f / (1.f + __expf(-z));
-  if constexpr (ACT == SIG_ACT_GELU) return 0.5f * erfcf(-z * kInvSqrt2);
+  if constexpr (ACT == SIG_ACT_SILU) return logistic(z);
+  if constexpr (ACT == SIG_ACT_GELU) return normal_cdf(z);
   if constexpr (ACT == SIG_ACT_GELU_TANH)
-    return 1.f / (1.f + __expf(-2.f * kGeluC * z * fmaf(kGeluA * z, z, 1.f)));
+    return logistic(2.f * kGeluC * z * fmaf(kGeluA * z, z, 1.f));
   return 1.f;
 }
 
@@ -291,7 +311,7 @@ __device__ __forceinline__ float act_value(float z, float p) {
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z, float p) {
   if constexpr (ACT == SIG_ACT_SILU) return p * fmaf(z, 1.f - p, 1.f);
-  if constexpr (ACT == SIG_ACT_GELU) return fmaf(z * kInvSqrt2Pi, __expf(-0.5f * z * z), p);
+  if constexpr (ACT == SIG_ACT_GELU) return fmaf(z * kInvSqrt2Pi, bell(z), p);
   if constexpr (ACT == SIG_ACT_GELU_TANH)   // beyond |z| = 20 p is 0 or 1 (and z^2 may overflow)
     return fabsf(z) > 20.f ? p : fmaf(z * p * (1.f - p), 2.f * kGeluC * fmaf(3.f * kGeluA * z, z, 1.f), p);
   return p;   // none, relu
@@ -310,6 +330,59 @@ __device__ __forceinline__ void with_act(int act, F&& f) {
 }
 
 __device__ __forceinline__ uint4 ld16(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
+
+// v[0 .. 8 G) = act(v + bias) for 8 G columns from `col` (columns from `cols` on
+// are left without the bias)
+template <bool BF, int G>
+__device__ __forceinline__ void epi_bias_act(float* v, const DenseArgs& a, int col) {
+  if (a.bias != nullptr) {
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+      if (col + 8 * j < a.cols) {
+        float b[8];
+        unpack8<BF>(b, ld16(a.bias + col + 8 * j));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * j + i] += b[i];
+      }
+  }
+  if (a.act != SIG_ACT_NONE)
+    with_act(a.act, [&](auto A) {
+#pragma unroll
+      for (int i = 0; i < 8 * G; ++i)
+        v[i] = act_value<decltype(A)::value>(v[i], act_share<decltype(A)::value>(v[i]));
+    });
+}
+
+// g <- act(g) u over n columns
+template <int n>
+__device__ __forceinline__ void epi_gated(float* g, const float* u, int act) {
+  with_act(act, [&](auto A) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) g[i] = act_value<decltype(A)::value>(g[i], act_share<decltype(A)::value>(g[i])) * u[i];
+  });
+}
+
+// dh -> (dg, du, h) over 8 columns
+template <bool BF>
+__device__ __forceinline__ void epi_grad8(const float* dh, const uint4& gv, const uint4& uv, int act,
+                                          uint4& dg, uint4& du, uint4& h) {
+  float g[8], u[8], a0[8], a1[8], a2[8];
+  unpack8<BF>(g, gv);
+  unpack8<BF>(u, uv);
+  with_act(act, [&](auto A) {
+    constexpr int ACT = decltype(A)::value;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float p = act_share<ACT>(g[i]), v = act_value<ACT>(g[i], p);
+      a0[i] = dh[i] * u[i] * act_slope<ACT>(g[i], p);
+      a1[i] = dh[i] * v;
+      a2[i] = v * u[i];
+    }
+  });
+  dg = pack8<BF>(a0);
+  du = pack8<BF>(a1);
+  h = pack8<BF>(a2);
+}
 
 // What the epilogue of 8 columns of a token reads besides the sums: the
 // residual, or g and u.  Loaded ahead of the sums.
@@ -341,18 +414,7 @@ __device__ __forceinline__ void finish8(float (&v)[8], const float (&w)[8], cons
                                         const DenseArgs& a, int mat, int row, int col) {
   const int64_t at = (int64_t)row * a.ldo + col;
   if constexpr (EPI == DENSE_LINEAR) {
-    if (a.bias != nullptr) {
-      float b[8];
-      unpack8<BF>(b, ld16(a.bias + col));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += b[i];
-    }
-    if (a.act != SIG_ACT_NONE)
-      with_act(a.act, [&](auto A) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          v[i] = act_value<decltype(A)::value>(v[i], act_share<decltype(A)::value>(v[i]));
-      });
+    epi_bias_act<BF, 1>(v, a, col);
     if (a.residual != nullptr) {
       float r[8];
       unpack8<BF>(r, e.x);
@@ -365,29 +427,14 @@ __device__ __forceinline__ void finish8(float (&v)[8], const float (&w)[8], cons
       store16(a.o[1] + at, pack8<BF>(v));
       store16(a.o[2] + at, pack8<BF>(w));
     }
-    with_act(a.act, [&](auto A) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = act_value<decltype(A)::value>(v[i], act_share<decltype(A)::value>(v[i])) * w[i];
-    });
+    epi_gated<8>(v, w, a.act);
     store16(a.o[0] + at, pack8<BF>(v));
   } else {
-    float g[8], u[8], dg[8], du[8], h[8];
-    unpack8<BF>(g, e.x);
-    unpack8<BF>(u, e.y);
-    with_act(a.act, [&](auto A) {
-      constexpr int ACT = decltype(A)::value;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float p = act_share<ACT>(g[i]), y = act_value<ACT>(g[i], p);
-        dg[i] = v[i] * u[i] * act_slope<ACT>(g[i], p);
-        du[i] = v[i] * y;
-        h[i] = y * u[i];
-      }
-    });
-    store16(a.o[0] + at, pack8<BF>(dg));
-    store16(a.o[1] + at, pack8<BF>(du));
-    store16(a.o[2] + at, pack8<BF>(h));
+    uint4 dg, du, h;
+    epi_grad8<BF>(v, e.x, e.y, a.act, dg, du, h);
+    store16(a.o[0] + at, dg);
+    store16(a.o[1] + at, du);
+    store16(a.o[2] + at, h);
   }
 }
 
@@ -488,77 +535,6 @@ __device__ __forceinline__ void weight_boxes(const DenseMaps& maps, const DenseA
   }
 }
 
-// v[0 .. 8 G) = act(v + bias) + residual for 8 G columns from `col` of `row`;
-// columns from `cols` on and rows from `rows` on are left without the two.
-template <bool BF, int G>
-__device__ __forceinline__ void epi_linear(float* v, const DenseArgs& a, int row, int col) {
-  uint4 res[G];
-  if (a.residual != nullptr) {
-#pragma unroll
-    for (int j = 0; j < G; ++j)
-      res[j] = row < a.rows && col + 8 * j < a.cols
-                   // plain load: Y may be the residual buffer itself
-                   ? *reinterpret_cast<const uint4*>(a.residual + (int64_t)row * a.ldr + col + 8 * j)
-                   : make_uint4(0, 0, 0, 0);
-  }
-  if (a.bias != nullptr) {
-#pragma unroll
-    for (int j = 0; j < G; ++j)
-      if (col + 8 * j < a.cols) {
-        float b[8];
-        unpack8<BF>(b, ld16(a.bias + col + 8 * j));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[8 * j + i] += b[i];
-      }
-  }
-  if (a.act != SIG_ACT_NONE)
-    with_act(a.act, [&](auto A) {
-#pragma unroll
-      for (int i = 0; i < 8 * G; ++i)
-        v[i] = act_value<decltype(A)::value>(v[i], act_share<decltype(A)::value>(v[i]));
-    });
-  if (a.residual != nullptr) {
-#pragma unroll
-    for (int j = 0; j < G; ++j) {
-      float r[8];
-      unpack8<BF>(r, res[j]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[8 * j + i] += r[i];
-    }
-  }
-}
-
-// g <- act(g) u over n columns
-template <int n>
-__device__ __forceinline__ void epi_gated(float* g, const float* u, int act) {
-  with_act(act, [&](auto A) {
-#pragma unroll
-    for (int i = 0; i < n; ++i) g[i] = act_value<decltype(A)::value>(g[i], act_share<decltype(A)::value>(g[i])) * u[i];
-  });
-}
-
-// dh -> (dg, du, h) over 8 columns
-template <bool BF>
-__device__ __forceinline__ void epi_grad8(const float* dh, const uint4& gv, const uint4& uv, int act,
-                                          uint4& dg, uint4& du, uint4& h) {
-  float g[8], u[8], a0[8], a1[8], a2[8];
-  unpack8<BF>(g, gv);
-  unpack8<BF>(u, uv);
-  with_act(act, [&](auto A) {
-    constexpr int ACT = decltype(A)::value;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float p = act_share<ACT>(g[i]), v = act_value<ACT>(g[i], p);
-      a0[i] = dh[i] * u[i] * act_slope<ACT>(g[i], p);
-      a1[i] = dh[i] * v;
-      a2[i] = v * u[i];
-    }
-  });
-  dg = pack8<BF>(a0);
-  du = pack8<BF>(a1);
-  h = pack8<BF>(a2);
-}
-
 // ---------------------------------------------------------------------------
 // Persistent CTA pairs: tiles of 256 tokens x 256 (or 128) accumulator columns
 //
@@ -571,19 +547,32 @@ __device__ __forceinline__ void epi_grad8(const float* dh, const uint4& gv, cons
 // 512 x 4096 x 4096 19.2 against 25.3 us.
 // ---------------------------------------------------------------------------
 constexpr int kPairThreads = 320;                  // 8 epilogue warps, one loads, one issues MMAs
-constexpr int kPairStages = 5;
+constexpr int kPairMaxStages = 5;
 constexpr uint32_t kOperand = kTile * kSlab * 2;   // 16 KB: 128 rows (or columns) x 64 K
 constexpr uint32_t kStoreBlock = 32 * 128;         // 32 rows x 64 columns; an epilogue warp has two
 constexpr int kGroupRows = 8;                      // row tiles walked together (L2 reuse of B)
 constexpr int kSmemPerCta = 227 * 1024, kSmemPerSm = 228 * 1024;   // a CTA costs 1 KB more than it asks for
 
-// After the ring (stage: 128 rows of A, then this CTA's half of the columns
-// of B) and the eight epilogue warps' store blocks.
+// Shared memory: the ring (stage: 128 rows of A, then this CTA's half of the
+// columns of B), the eight epilogue warps' blocks, the barriers.  A warp's
+// blocks hold what it reads (residual; g and u), brought by TMA ahead of the
+// accumulator, and in its place what it stores: two of 32 rows x 64 columns, or
+// for DENSE_GRAD two sets of three of 32 x 32, at the price of a ring stage.
+// Lanes reading 16 bytes of 32 different rows straight from global memory
+// instead took 41 of 147 us of the gradient's first product at 2048 x 4096 x 11008.
+template <int EPI>
+struct PairCfg {
+  static constexpr int kStages = EPI == DENSE_GRAD ? 4 : 5;
+  static constexpr uint32_t kSet = EPI == DENSE_GRAD ? 3 * 2048 : kStoreBlock;   // bytes of one of the two
+  static constexpr uint32_t kWarpBytes = 2 * kSet;
+};
+
 struct PairBars {
-  unsigned long long full[kPairStages];         // used in the leader
-  unsigned long long empty[kPairStages];
+  unsigned long long full[kPairMaxStages];         // used in the leader
+  unsigned long long empty[kPairMaxStages];
   unsigned long long acc_full[2], acc_empty[2];    // acc_empty used in the leader
   unsigned long long done;
+  unsigned long long extra[8][2];                  // per epilogue warp: what it reads, per set
   uint32_t tmem_base;
   int abort_flag;
   int consumed;
@@ -606,27 +595,26 @@ __device__ __forceinline__ TilePos tile_at(int t, const DenseArgs& a) {
   return {g0 + r % gs, mat, (n - mat * a.tn) * 256 + (half ? (t - a.whole) % 2 * 128 : 0), half ? 128 : 256};
 }
 
-// Write 32 rows x 32 columns (64 bytes a lane) into a store block at column
-// 32 * part, in the 128-byte swizzled order of a store map 64 columns wide ...
-__device__ __forceinline__ void stage_words(uint32_t block, int lane, int part, const uint4 (&p)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t addr = block + (uint32_t)lane * 128u + (uint32_t)(((part * 4 + j) ^ (lane & 7)) << 4);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(p[j].x), "r"(p[j].y),
-                 "r"(p[j].z), "r"(p[j].w)
-                 : "memory");
-  }
+// Where lane's (row's) 16-byte chunk j lies in a block: 64 columns wide, in the
+// 128-byte swizzled order of its tensor map, or 32 wide in the 64-byte one.
+__device__ __forceinline__ uint32_t wide_at(uint32_t block, int lane, int j) {
+  return block + (uint32_t)lane * 128u + (uint32_t)((j ^ (lane & 7)) << 4);
+}
+__device__ __forceinline__ uint32_t narrow_at(uint32_t block, int lane, int j) {
+  return block + (uint32_t)lane * 64u + (uint32_t)((j ^ ((lane >> 1) & 3)) << 4);
 }
 
-// ... or into a 2 KB block in the 64-byte swizzled order of a map 32 columns wide.
-__device__ __forceinline__ void stage_narrow(uint32_t block, int lane, const uint4 (&p)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t addr = block + (uint32_t)lane * 64u + (uint32_t)((j ^ ((lane >> 1) & 3)) << 4);
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(p[j].x), "r"(p[j].y),
-                 "r"(p[j].z), "r"(p[j].w)
-                 : "memory");
-  }
+__device__ __forceinline__ void sts16(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
 // A block is free once the stores from it have read it; `N` later ones may be on their way.
@@ -652,10 +640,11 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  constexpr int S = kPairStages;
+  using Cfg = PairCfg<EPI>;
+  constexpr int S = Cfg::kStages;
   constexpr uint32_t stage_bytes = 2 * kOperand;   // 128 rows of A and up to 128 columns of B
   uint8_t* blocks = ring + (size_t)S * stage_bytes;
-  PairBars& sm = *reinterpret_cast<PairBars*>(blocks + 16 * kStoreBlock);
+  PairBars& sm = *reinterpret_cast<PairBars*>(blocks + 8 * Cfg::kWarpBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
@@ -663,8 +652,8 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
   volatile int* abort_flag = &sm.abort_flag;
   pdl_trigger();
 
-  if (warp == 9 && lane < 7)
-    prefetch_map(lane < 2 ? &maps.a[lane] : lane < 4 ? &maps.b[lane - 2] : &maps.o[lane - 4]);
+  if (warp == 9 && lane < 9)
+    prefetch_map(lane < 2 ? &maps.a[lane] : lane < 4 ? &maps.b[lane - 2] : lane < 7 ? &maps.o[lane - 4] : &maps.r[lane - 7]);
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&sm.full[s]), 1);
@@ -675,6 +664,7 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
       mbar_init(smem_u32(&sm.acc_empty[s]), 16);   // the epilogue warps of both CTAs
     }
     mbar_init(smem_u32(&sm.done), 1);
+    for (int w = 0; w < 16; ++w) mbar_init(smem_u32(&sm.extra[w / 2][w % 2]), 1);
     sm.abort_flag = 0;
     sm.consumed = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -773,27 +763,47 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
     }
   } else {   // ---- epilogue: eight warps, each 32 rows x half of the columns ----
     const int q = warp & 3, half = warp >> 2;
-    const uint32_t store = smem_u32(blocks) + (uint32_t)warp * 2 * kStoreBlock;
+    const uint32_t store = smem_u32(blocks) + (uint32_t)warp * Cfg::kWarpBytes;
     const uint32_t empty0 = map_to_rank(smem_u32(&sm.acc_empty[0]), 0);
     const uint32_t empty1 = map_to_rank(smem_u32(&sm.acc_empty[1]), 0);
+    const bool reads = EPI == DENSE_GRAD || (EPI == DENSE_LINEAR && args.residual != nullptr);
     int count = 0;
-    uint32_t next = 0;   // the store block written next: 0 or kStoreBlock
+    uint32_t set = 0;         // the set of blocks used next
+    uint32_t extra_ph = 0;    // bit s: parity of extra[s]'s next phase
+    uint32_t coming = 0;      // bit s: a read into set s is on its way
+    // start the reads of a piece (64 columns; DENSE_GRAD 32) into set s; one lane
+    auto fetch = [&](uint32_t s, int col, int row0) {
+      if (row0 >= args.rows || col >= args.cols) return;
+      coming |= 1u << s;
+      if (lane == 0) {
+        const uint32_t bar = smem_u32(&sm.extra[warp][s]), to = store + s * Cfg::kSet;
+        mbar_expect_tx(bar, 4096u);
+        tma_load_2d(to, &maps.r[0], col, row0, bar);
+        if constexpr (EPI == DENSE_GRAD) tma_load_2d(to + 2048u, &maps.r[1], col, row0, bar);
+      }
+    };
+    // wait for them; false when a wait gave up
+    auto fetched = [&](uint32_t s) {
+      const bool ok = __all_sync(kFull, wait_bounded(smem_u32(&sm.extra[warp][s]), (extra_ph >> s) & 1u,
+                                                     abort_flag, limit));
+      if (ok) {
+        extra_ph ^= 1u << s;
+        coming &= ~(1u << s);
+      }
+      return ok;
+    };
     for (int t = pair; t < args.items; t += pairs, ++count) {
       const TilePos p = tile_at(t, args);
-      const int row0 = p.m * 256 + (int)rank * 128 + q * 32, row = row0 + lane;
-      const int blocks_of_warp = p.bn / 128;   // blocks of 64 columns (DENSE_LINEAR, DENSE_GRAD)
-      const int slot = count & 1;
-      uint4 gn[4], un[4];   // DENSE_GRAD: g and u of this row's next 32 columns
-      auto fetch_gu = [&](int r, int col) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const bool in = r < args.rows && col + 8 * j < args.cols;
-          const int64_t at = (int64_t)r * args.cols + col + 8 * j;
-          gn[j] = in ? ld16(args.g + at) : make_uint4(0, 0, 0, 0);
-          un[j] = in ? ld16(args.u + at) : make_uint4(0, 0, 0, 0);
-        }
-      };
-      if constexpr (EPI == DENSE_GRAD) fetch_gu(row, p.n + half * (p.bn / 2));
+      const int row0 = p.m * 256 + (int)rank * 128 + q * 32;
+      const int blocks_of_warp = p.bn / 128;   // pieces of 64 columns (DENSE_LINEAR, DENSE_GRAD)
+      const int slot = count & 1, c_warp = half * (p.bn / 2), col_warp = p.n + c_warp;
+      constexpr int kPiece = EPI == DENSE_GRAD ? 32 : 64;
+      const int pieces = blocks_of_warp * 64 / kPiece;
+      if (reads) {   // the first two pieces, before the accumulator is complete
+        stage_wait<0>(lane);
+        fetch(set, col_warp, row0);
+        if (pieces > 1) fetch(set ^ 1u, col_warp + kPiece, row0);
+      }
       // one verdict for the warp: the tensor-memory loads below need all its lanes
       if (!__all_sync(kFull, wait_bounded(smem_u32(&sm.acc_full[slot]), (uint32_t)(count >> 1) & 1u,
                                           abort_flag, limit)))
@@ -805,104 +815,120 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
         __syncwarp();
         if (lane == 0) arrive_remote(slot ? empty1 : empty0);
       };
+      bool go = true;
       if constexpr (EPI == DENSE_LINEAR) {
 #pragma unroll 1
-        for (int blk = 0; blk < blocks_of_warp; ++blk) {
-          const int c = half * (p.bn / 2) + blk * 64, col = p.n + c;
+        for (int blk = 0; blk < pieces; ++blk, set ^= 1u) {
+          const int c = c_warp + blk * 64, col = p.n + c;
+          const uint32_t to = store + set * Cfg::kSet;
+          if (!reads)
+            stage_wait<1>(lane);
+          else if ((coming >> set) & 1u)
+            go = fetched(set) && go;
 #pragma unroll
           for (int part = 0; part < 2; ++part) {
             uint32_t r[32];
             tmem_start32(r, acc + (uint32_t)(c + part * 32));
             tmem_wait32(r);
-            if (blk == blocks_of_warp - 1 && part == 1) release();
+            if (blk == pieces - 1 && part == 1) release();
             float v[32];
             as_floats(v, r);
-            if (!args.plain) epi_linear<BF, 4>(v, args, row, col + part * 32);
-            uint4 w[4];
+            if (!args.plain) {
+              epi_bias_act<BF, 4>(v, args, col + part * 32);
+              if (reads) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = pack8<BF>(*reinterpret_cast<float(*)[8]>(&v[8 * j]));
-            if (part == 0) stage_wait<1>(lane);
-            stage_words(store + next, lane, part, w);
+                for (int j = 0; j < 4; ++j) {
+                  float x[8];
+                  unpack8<BF>(x, lds16(wide_at(to, lane, part * 4 + j)));
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) v[8 * j + i] += x[i];
+                }
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              sts16(wide_at(to, lane, part * 4 + j), pack8<BF>(*reinterpret_cast<float(*)[8]>(&v[8 * j])));
           }
-          stage_store(store + next, lane, &maps.o[p.mat], col, row0, args);
-          next ^= kStoreBlock;
+          stage_store(to, lane, &maps.o[p.mat], col, row0, args);
         }
       } else if constexpr (EPI == DENSE_GATED) {
-        // accumulator columns [0, p.bn / 2) are g, the others u; 64 hidden columns a
+        // accumulator columns [0, bn / 2) are g, the others u; 64 hidden columns a
         // warp (with bn 128 there is only work for the first of a quarter's two)
         const int c = half * 64, col = p.n / 2 + c;
         if (c >= p.bn / 2) {
           release();
           continue;
         }
-        uint4 w[3][2][4];
-#pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          uint32_t rg[32], ru[32];
-          tmem_start32(rg, acc + (uint32_t)(c + part * 32));
-          tmem_start32(ru, acc + (uint32_t)(p.bn / 2 + c + part * 32));
-          tmem_wait32(rg);
-          tmem_wait32(ru);
-          if (part == 1) release();
-          float g[32], u[32];
-          as_floats(g, rg);
-          as_floats(u, ru);
-          if (args.outs == 3) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              w[1][part][j] = pack8<BF>(*reinterpret_cast<float(*)[8]>(&g[8 * j]));
-              w[2][part][j] = pack8<BF>(*reinterpret_cast<float(*)[8]>(&u[8 * j]));
-            }
-          }
-          epi_gated<32>(g, u, args.act);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[0][part][j] = pack8<BF>(*reinterpret_cast<float(*)[8]>(&g[8 * j]));
-        }
-#pragma unroll
-        for (int out = 0; out < 3; ++out) {
-          if (out >= args.outs) break;
+#pragma unroll 1
+        for (int out = 0; out < args.outs; ++out, set ^= 1u) {   // h, then g and u themselves
+          const uint32_t to = store + set * Cfg::kSet;
           stage_wait<1>(lane);
-          stage_words(store + next, lane, 0, w[out][0]);
-          stage_words(store + next, lane, 1, w[out][1]);
-          stage_store(store + next, lane, &maps.o[out], col, row0, args);
-          next ^= kStoreBlock;
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {
+            uint32_t r[32];
+            tmem_start32(r, acc + (uint32_t)(c + part * 32 + (out == 2 ? p.bn / 2 : 0)));
+            float v[32];
+            if (out == 0) {
+              uint32_t ru[32];
+              tmem_start32(ru, acc + (uint32_t)(p.bn / 2 + c + part * 32));
+              tmem_wait32(r);
+              tmem_wait32(ru);
+              if (args.outs == 1 && part == 1) release();
+              float u[32];
+              as_floats(v, r);
+              as_floats(u, ru);
+              epi_gated<32>(v, u, args.act);
+            } else {
+              tmem_wait32(r);
+              if (out == 2 && part == 1) release();
+              as_floats(v, r);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              sts16(wide_at(to, lane, part * 4 + j), pack8<BF>(*reinterpret_cast<float(*)[8]>(&v[8 * j])));
+          }
+          stage_store(to, lane, &maps.o[out], col, row0, args);
         }
       } else {
-        // 32 columns at a time; g and u of the next 32 are on their way meanwhile,
-        // those of the first since before the accumulator was complete
 #pragma unroll 1
-        for (int i = 0; i < 2 * blocks_of_warp; ++i) {
-          const int c = half * (p.bn / 2) + i * 32, col = p.n + c;
-          uint4 gv[4], uv[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            gv[j] = gn[j];
-            uv[j] = un[j];
-          }
+        for (int i = 0; i < pieces; ++i, set ^= 1u) {
+          const int c = c_warp + i * 32, col = p.n + c;
+          const uint32_t to = store + set * Cfg::kSet;
+          if ((coming >> set) & 1u) go = fetched(set) && go;
           uint32_t r[32];
           tmem_start32(r, acc + (uint32_t)c);
-          if (i < 2 * blocks_of_warp - 1) fetch_gu(row, col + 32);
           tmem_wait32(r);
-          if (i == 2 * blocks_of_warp - 1) release();
+          if (i == pieces - 1) release();
           float v[32];
           as_floats(v, r);
-          uint4 w[3][4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            epi_grad8<BF>(&v[8 * j], gv[j], uv[j], args.act, w[0][j], w[1][j], w[2][j]);
-          stage_wait<0>(lane);
-#pragma unroll
-          for (int out = 0; out < 3; ++out) stage_narrow(store + out * 2048u, lane, w[out]);
+          for (int j = 0; j < 4; ++j) {   // dg and du take the places of g and u, h the third
+            const uint32_t at = narrow_at(to, lane, j);
+            uint4 dg, du, h;
+            epi_grad8<BF>(&v[8 * j], lds16(at), lds16(at + 2048u), args.act, dg, du, h);
+            sts16(at, dg);
+            sts16(at + 2048u, du);
+            sts16(at + 4096u, h);
+          }
+          if (i > 0 && i + 1 < pieces) {   // the next piece goes where the last one was
+            stage_wait<0>(lane);
+            fetch(set ^ 1u, col + 32, row0);
+          }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
             if (row0 < args.rows && col < args.cols)
-              for (int out = 0; out < 3; ++out) tma_store_2d(&maps.o[out], store + out * 2048u, col, row0);
+              for (int out = 0; out < 3; ++out) tma_store_2d(&maps.o[out], to + out * 2048u, col, row0);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
         }
       }
+      if (!go) break;
     }
+    // after a give-up: reads on their way land before shared memory goes
+    for (uint32_t s = 0; s < 2; ++s)
+      if ((coming >> s) & 1u) wait_drain(smem_u32(&sm.extra[warp][s]), (extra_ph >> s) & 1u);
+    __syncwarp();
     // the outputs are written before the CTA ends
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
@@ -1195,8 +1221,9 @@ cudaError_t launch_cluster(dim3 grid, int threads, int cluster, size_t smem, cud
 
 template <bool A_MN, bool B_K, int EPI, bool BF>
 cudaError_t launch_pair_kernel(const DenseMaps& maps, const DenseArgs& args, cudaStream_t stream) {
-  constexpr int kStageBytes = 2 * (int)kOperand;
-  constexpr int kSmem = kPairStages * kStageBytes + 16 * (int)kStoreBlock + (int)sizeof(PairBars) + 1024;
+  using Cfg = PairCfg<EPI>;
+  constexpr int kSmem =
+      Cfg::kStages * 2 * (int)kOperand + 8 * (int)Cfg::kWarpBytes + (int)sizeof(PairBars) + 1024;
   static_assert(kSmem <= kSmemPerCta, "ring, store blocks and barriers fit an SM");
   const int pairs = std::min(args.items, kNumSMs / 2);
   return launch_cluster<&dense_pair_kernel<A_MN, B_K, EPI, BF>>(dim3(2 * pairs), kPairThreads, 2, kSmem, stream,
@@ -1285,16 +1312,23 @@ cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream) {
     if (!(d.b_k ? map16(&maps.b[i], d.b[i], d.K, d.cols, d.ldb, p.pair ? 64 : kTile)
                 : map16(&maps.b[i], d.b[i], d.cols, d.K, d.ldb, kSlab)))
       return cudaErrorInvalidValue;
-  if (p.pair)   // the pair kernel stores its outputs with TMA
-    for (int i = 0; i < 3; ++i)
-      if (d.o[i] != nullptr && !map16(&maps.o[i], d.o[i], d.cols, d.rows, d.ldo, 32, d.epi == DENSE_GRAD ? 32 : 64))
-        return cudaErrorInvalidValue;
-  // the kernels prefetch every map: the unused ones repeat the first
+  // the kernels prefetch every map: the unused ones repeat another
   if (n_a < 2) maps.a[1] = maps.a[0];
   if (n_b < 2) maps.b[1] = maps.b[0];
-  if (p.pair)
-    for (int i = 1; i < 3; ++i)
-      if (d.o[i] == nullptr) maps.o[i] = maps.o[0];
+  if (p.pair) {   // the pair kernel reads its other inputs and stores its outputs with TMA
+    const int width = d.epi == DENSE_GRAD ? 32 : 64;
+    const uint16_t* r[2] = {d.epi == DENSE_GRAD ? d.g : d.residual, d.epi == DENSE_GRAD ? d.u : nullptr};
+    for (int i = 0; i < 3; ++i)
+      if (d.o[i] == nullptr)
+        maps.o[i] = maps.o[0];
+      else if (!map16(&maps.o[i], d.o[i], d.cols, d.rows, d.ldo, 32, width))
+        return cudaErrorInvalidValue;
+    for (int i = 0; i < 2; ++i)
+      if (r[i] == nullptr)
+        maps.r[i] = maps.o[0];
+      else if (!map16(&maps.r[i], r[i], d.cols, d.rows, d.epi == DENSE_GRAD ? d.cols : d.ldr, 32, width))
+        return cudaErrorInvalidValue;
+  }
   return d.bf16 ? launch_typed<true>(d, p, maps, a, stream) : launch_typed<false>(d, p, maps, a, stream);
 }
 
