@@ -487,6 +487,78 @@ def test_a_training_step_through_the_block(sig):
         within(v, w, tol, k)
 
 
+def test_outputs_beyond_32_bit_offsets(sig):
+    """More than 2^31 outputs: 270 000 tokens to 8192 columns, the last rows and
+    a sample of the others against float64."""
+    import torch
+    rows, K, N = 270_000, 40, 8192
+    X, W = normal(120, rows, K), normal(121, K, N, scale=K ** -0.5)
+    b = normal(122, N)
+    Y = sig.linear_act(X, W, bias=b, act=sig.ACT_RELU)
+    at = torch.cat([torch.randint(0, rows, (400,), generator=torch.Generator().manual_seed(5)),
+                    torch.tensor([0, 262143, 262144, rows - 1])]).cuda()
+    z, e = product(X[at], W)
+    z = z + b.double()
+    y, e = z.clamp(min=0.0), e + U * z.abs()
+    within(Y[at], y, rounding(y, e, "fp16"), "270000 x 40 x 8192")
+
+
+# the listed kernels' borders: one block of tokens and several in the few-token
+# kernel, its join in its own place (to 64 tokens) and in the ring's, odd numbers
+# of parts along K, whole and half tiles of the pair kernel, one and many waves
+@pytest.mark.parametrize("rows,K,N", [
+    (15, 64, 4096), (17, 640, 128), (48, 1024, 384), (63, 4096, 1000), (65, 1024, 136), (66, 11008, 136),
+    (112, 2048, 2816), (176, 5632, 512), (257, 4096, 256), (515, 5632, 1024), (640, 1024, 2816),
+    (1024, 520, 1024), (1025, 64, 9728), (1281, 320, 5000), (9473, 128, 520)])
+def test_linear_kernel_borders(sig, rows, K, N):
+    for dtype in TYPES:
+        check_linear(sig, rows, K, N, dtype, "gelu", True, True, seed=rows)
+        check_linear(sig, rows, K, N, dtype, "none", False, False, seed=rows + 7)
+
+
+@pytest.mark.parametrize("rows", [600, 1500])
+def test_a_wait_that_gives_up_lets_the_epilogues_reads_land(sig, rows):
+    """The same for the epilogues that read while they wait: the residual, and g
+    and u of the backward pass."""
+    import torch
+    args = backward_inputs(rows, 256, 1096, "fp16", seed=130)
+    R = normal(140, rows, 1096)
+    W = args[4]
+    want = [sig.linear_act(args[1], W, residual=R), *sig.gated_mlp_backward(*args)]
+    assert sig.take_device_error() == 0
+    try:
+        sig.set_wait_limit(64)
+        sig.linear_act(args[1], W, residual=R)
+        sig.gated_mlp_backward(*args)
+        torch.cuda.synchronize()
+        assert sig.take_device_error() != 0
+    finally:
+        sig.set_wait_limit(0)
+    got = [sig.linear_act(args[1], W, residual=R), *sig.gated_mlp_backward(*args)]
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    assert sig.take_device_error() == 0
+
+
+@pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu", "relu"])
+def test_activations_and_slopes_over_their_range(sig, act):
+    """Every activation and its slope at values from deep in one tail to the
+    other: an identity weight, so that the kernel's sum is the argument itself."""
+    import torch
+    n = 1024
+    for dtype in TYPES:
+        z = torch.linspace(-12.0, 12.0, 512 * n, dtype=torch.float64, device="cuda").reshape(512, n).to(dt(dtype))
+        eye = torch.eye(n, dtype=dt(dtype), device="cuda")
+        a, slope = act64(act, z.double())
+        err = 2.0 ** -20 * z.double().abs().clamp(min=1.0)
+        within(sig.linear_act(z, eye, act=code(sig, act)), a, rounding(a, err, dtype), "act")
+        within(sig.linear_act(z[:7], eye, act=code(sig, act)), a[:7], rounding(a, err, dtype)[:7], "act, few")
+        # dX with dh = 1 (WdT = I, dY = 1), u = 1 and unit gate weights is act'(g) + act(g) u'
+        one, zero = torch.ones_like(z), torch.zeros(n, n, dtype=dt(dtype), device="cuda")
+        dX = sig.gated_mlp_backward(one, z, z, one, eye, zero, eye, act=code(sig, act), want_weights=False)[0]
+        e1 = rounding(slope, err, dtype)             # dg rounded to the type, then dX = dg
+        within(dX, slope, rounding(slope, e1, dtype), "slope")
+
+
 @pytest.mark.parametrize("rows", [4, 600])
 def test_a_wait_that_gives_up_is_reported(sig, rows):
     """With the wait limit at a few cycles the first wait for data gives up; the
