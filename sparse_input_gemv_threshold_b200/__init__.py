@@ -546,7 +546,7 @@ def _elsewhere(X, stream):
     return torch.cuda.stream(s)
 
 
-def _matrix(t, name, X, rows, cols, contiguous=False):
+def _matrix(t, name, X, rows, cols):
     """Check a 2-D tensor of X's type and device; returns its row stride."""
     if t.dtype is not X.dtype or t.get_device() != X.get_device():
         raise TypeError(f"{name} must be {X.dtype} on {X.device}, got {t.dtype} on {t.device}")
@@ -555,11 +555,18 @@ def _matrix(t, name, X, rows, cols, contiguous=False):
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    if rows <= 1:   # a single row has no stride of its own: any that the library accepts
-        return -(-cols // 8) * 8
-    if contiguous and ld != cols:
+    # a single row has no stride of its own: any that the library accepts
+    return ld if rows > 1 else -(-cols // 8) * 8
+
+
+def _whole(t, name, X, rows, cols):
+    """Check a contiguous 2-D tensor of X's type and device."""
+    if t.dtype is not X.dtype or t.get_device() != X.get_device():
+        raise TypeError(f"{name} must be {X.dtype} on {X.device}, got {t.dtype} on {t.device}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return ld
 
 
 def _block(X, name):
@@ -592,7 +599,7 @@ def linear_act(X, WT, bias=None, act: int = ACT_NONE, residual=None, Y=None, str
             return linear_act(X, WT, bias, act, residual, Y)
     N = _width(WT, "WT")
     ldx = _matrix(X, "X", X, rows, K)
-    _matrix(WT, "WT", X, K, N, True)
+    _whole(WT, "WT", X, K, N)
     ldr = ldy = N
     b = r = None
     if bias is not None:
@@ -602,7 +609,7 @@ def linear_act(X, WT, bias=None, act: int = ACT_NONE, residual=None, Y=None, str
     if residual is not None:
         ldr, r = _matrix(residual, "residual", X, rows, N), residual.data_ptr()
     if Y is None:
-        Y = X.new_empty((rows, N))
+        Y = X.new_empty((rows, N)) if N != K else torch.empty_like(X)
     else:
         ldy = _matrix(Y, "Y", X, rows, N)
     _check("linear_act", _lib.linear_act(
@@ -626,16 +633,16 @@ def gated_mlp(X, WgT, WuT, WdT, act: int = ACT_SILU, residual=None, Y=None, h_ou
             return gated_mlp(X, WgT, WuT, WdT, act, residual, Y, h_out, g_out, u_out)
     f = _width(WgT, "WgT")
     ldx = _matrix(X, "X", X, rows, m)
-    _matrix(WgT, "WgT", X, m, f, True)
-    _matrix(WuT, "WuT", X, m, f, True)
-    _matrix(WdT, "WdT", X, f, m, True)
+    _whole(WgT, "WgT", X, m, f)
+    _whole(WuT, "WuT", X, m, f)
+    _whole(WdT, "WdT", X, f, m)
     ldr = _matrix(residual, "residual", X, rows, m) if residual is not None else m
     for name, t in (("h_out", h_out), ("g_out", g_out), ("u_out", u_out)):
         if t is not None:
-            _matrix(t, name, X, rows, f, True)
+            _whole(t, name, X, rows, f)
     ldy = m
     if Y is None:
-        Y = X.new_empty((rows, m))
+        Y = torch.empty_like(X)
     else:
         ldy = _matrix(Y, "Y", X, rows, m)
     ws, n = None, 0
@@ -665,24 +672,25 @@ def gated_mlp_backward(dY, X, g, u, WgT, WuT, WdT, act: int = ACT_SILU, dX=None,
     f = _width(WgT, "WgT")
     ldx = _matrix(X, "X", X, rows, m)
     lddy = _matrix(dY, "dY", X, rows, m)
-    _matrix(g, "g", X, rows, f, True)
-    _matrix(u, "u", X, rows, f, True)
-    _matrix(WgT, "WgT", X, m, f, True)
-    _matrix(WuT, "WuT", X, m, f, True)
-    _matrix(WdT, "WdT", X, f, m, True)
+    _whole(g, "g", X, rows, f)
+    _whole(u, "u", X, rows, f)
+    _whole(WgT, "WgT", X, m, f)
+    _whole(WuT, "WuT", X, m, f)
+    _whole(WdT, "WdT", X, f, m)
     lddx = m
     if not want_x:
         dX = None
     elif dX is None:
-        dX = X.new_empty((rows, m))
+        dX = torch.empty_like(X)
     else:
         lddx = _matrix(dX, "dX", X, rows, m)
     if want_weights:
-        given = ((dWgT, "dWgT", m, f), (dWuT, "dWuT", m, f), (dWdT, "dWdT", f, m))
-        for t, name, r, c in given:
+        for t, name, r, c in ((dWgT, "dWgT", m, f), (dWuT, "dWuT", m, f), (dWdT, "dWdT", f, m)):
             if t is not None:
-                _matrix(t, name, X, r, c, True)
-        dWgT, dWuT, dWdT = (X.new_empty((r, c)) if t is None else t for t, _, r, c in given)
+                _whole(t, name, X, r, c)
+        dWgT = torch.empty_like(WgT) if dWgT is None else dWgT
+        dWuT = torch.empty_like(WuT) if dWuT is None else dWuT
+        dWdT = torch.empty_like(WdT) if dWdT is None else dWdT
     else:
         dWgT = dWuT = dWdT = None
     n = workspace_bytes(OP_GATED_BACKWARD, m, f, rows)

@@ -595,25 +595,23 @@ int gated_mlp_backward(const uint16_t* dY, int64_t lddy, const uint16_t* X, int6
     x.o[0] = dX; x.ldo = lddx;
     if (launch_dense(x, st) != cudaSuccess) return SIG_ERR_CUDA;
   }
-  if (dWgT != nullptr) {   // dWgT = X^T dg and dWuT = X^T du, one launch
-    DenseGemm w;
-    w.bf16 = bf16;
-    w.rows = d_model; w.cols = d_ff; w.K = rows;
-    w.a_mn = true; w.a[0] = X; w.lda = ldx;
-    w.mats = 2; w.b[0] = dg; w.b[1] = du; w.ldb = d_ff;
-    w.o[0] = dWgT; w.o[1] = dWuT; w.ldo = d_ff;
-    if (launch_dense(w, st) != cudaSuccess) return SIG_ERR_CUDA;
+  DenseGemm up;   // dWgT = X^T dg and dWuT = X^T du
+  up.bf16 = bf16;
+  up.rows = d_model; up.cols = d_ff; up.K = rows;
+  up.a_mn = true; up.a[0] = X; up.lda = ldx;
+  up.mats = 2; up.b[0] = dg; up.b[1] = du; up.ldb = d_ff;
+  up.o[0] = dWgT; up.o[1] = dWuT; up.ldo = d_ff;
+  DenseGemm down;   // dWdT = h^T dY
+  down.bf16 = bf16;
+  down.rows = d_ff; down.cols = d_model; down.K = rows;
+  down.a_mn = true; down.a[0] = h; down.lda = d_ff;
+  down.b[0] = dY; down.ldb = lddy;
+  down.o[0] = dWdT; down.ldo = d_model;
+  if (dWgT != nullptr) {   // one launch for all that is wanted
+    up.also = dWdT != nullptr ? &down : nullptr;
+    return cuda_status(launch_dense(up, st));
   }
-  if (dWdT != nullptr) {   // dWdT = h^T dY
-    DenseGemm w;
-    w.bf16 = bf16;
-    w.rows = d_ff; w.cols = d_model; w.K = rows;
-    w.a_mn = true; w.a[0] = h; w.lda = d_ff;
-    w.b[0] = dY; w.ldb = lddy;
-    w.o[0] = dWdT; w.ldo = d_model;
-    if (launch_dense(w, st) != cudaSuccess) return SIG_ERR_CUDA;
-  }
-  return SIG_OK;
+  return dWdT != nullptr ? cuda_status(launch_dense(down, st)) : SIG_OK;
 }
 
 int sig_set_wait_limit(long long cycles) {

@@ -36,13 +36,14 @@ constexpr int kSlab = 64;       // K of one stage: a 128-byte swizzle row of 16-
 constexpr uint32_t kBlock = kSlab * 128;   // 64 rows of 128 bytes
 
 struct DenseMaps {
-  CUtensorMap a[2], b[2], o[3], r[2];   // r: the residual, or g and u
+  CUtensorMap a[2], b[3], o[3], r[2];   // r: the residual, or g and u
 };
 
 struct DenseArgs {
   int rows, cols;      // rows (tokens) and columns of one output
   int kb0, kbt;        // K stages of the first segment, of both
   int tm, tn;          // tiles down, and across one weight
+  int rows2, cols2, tm2, tn2;   // pair kernel: the second product of the launch (weight 2), if any
   int whole, items;    // pair kernel: tiles taken whole, and all items of the walk
   int mats;
   int outs;            // outputs to store (DENSE_GATED: 1, or 3 with g and u)
@@ -583,16 +584,23 @@ struct PairBars {
 struct TilePos {
   int m, mat, n;   // row tile, weight, accumulator column
   int bn;          // 256 or 128
+  int rows, cols;  // of the output that the tile belongs to
 };
 
+// Row tiles are walked in groups, so that a group's tiles share their columns' B.
 __device__ __forceinline__ TilePos tile_at(int t, const DenseArgs& a) {
   const int half = t < a.whole ? 0 : 1;
-  const int u = half ? a.whole + (t - a.whole) / 2 : t;
-  const int tn_all = a.tn * a.mats, per = kGroupRows * tn_all;
+  int u = half ? a.whole + (t - a.whole) / 2 : t;
+  const int first = a.tm * a.tn * a.mats;
+  const bool also = u >= first;              // a tile of the second product
+  if (also) u -= first;
+  const int tm = also ? a.tm2 : a.tm, tn = also ? a.tn2 : a.tn;
+  const int per = kGroupRows * (also ? tn : tn * a.mats);
   const int g0 = u / per * kGroupRows, r = u % per;
-  const int gs = min(kGroupRows, a.tm - g0);
-  const int n = r / gs, mat = n / a.tn;
-  return {g0 + r % gs, mat, (n - mat * a.tn) * 256 + (half ? (t - a.whole) % 2 * 128 : 0), half ? 128 : 256};
+  const int gs = min(kGroupRows, tm - g0);
+  const int n = r / gs, mat = n / tn;
+  return {g0 + r % gs, also ? 2 : mat, (n - mat * tn) * 256 + (half ? (t - a.whole) % 2 * 128 : 0),
+          half ? 128 : 256, also ? a.rows2 : a.rows, also ? a.cols2 : a.cols};
 }
 
 // Where lane's (row's) 16-byte chunk j lies in a block: 64 columns wide, in the
@@ -625,11 +633,11 @@ __device__ __forceinline__ void stage_wait(int lane) {
 }
 
 __device__ __forceinline__ void stage_store(uint32_t block, int lane, const CUtensorMap* map, int col,
-                                            int row, const DenseArgs& a) {
+                                            int row, const TilePos& p) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   __syncwarp();
   if (lane == 0) {
-    if (row < a.rows && col < a.cols) tma_store_2d(map, block, col, row);   // the map clips the rest
+    if (row < p.rows && col < p.cols) tma_store_2d(map, block, col, row);   // the map clips the rest
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
 }
@@ -652,8 +660,11 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
   volatile int* abort_flag = &sm.abort_flag;
   pdl_trigger();
 
-  if (warp == 9 && lane < 9)
-    prefetch_map(lane < 2 ? &maps.a[lane] : lane < 4 ? &maps.b[lane - 2] : lane < 7 ? &maps.o[lane - 4] : &maps.r[lane - 7]);
+  if (warp == 9 && lane < 10)
+    prefetch_map(lane < 2   ? &maps.a[lane]
+                 : lane < 5 ? &maps.b[lane - 2]
+                 : lane < 8 ? &maps.o[lane - 5]
+                            : &maps.r[lane - 8]);
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(smem_u32(&sm.full[s]), 1);
@@ -700,7 +711,7 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
         if (!go) break;
         const int seg = kb >= args.kb0 ? 1 : 0;
         const int k = (kb - (seg ? args.kb0 : 0)) * kSlab;
-        const CUtensorMap* ma = &maps.a[seg];
+        const CUtensorMap* ma = &maps.a[A_MN ? p.mat >> 1 : seg];   // A_MN: one segment, the second product's A
         const CUtensorMap* mb = &maps.b[EPI == DENSE_GATED ? (int)rank : seg | p.mat];
         const uint32_t fb = full0 + (uint32_t)s * 8u;
         const uint32_t a0 = smem_u32(ring) + (uint32_t)s * stage_bytes, b0 = a0 + kOperand;
@@ -849,7 +860,7 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
             for (int j = 0; j < 4; ++j)
               sts16(wide_at(to, lane, part * 4 + j), pack8<BF>(*reinterpret_cast<float(*)[8]>(&v[8 * j])));
           }
-          stage_store(to, lane, &maps.o[p.mat], col, row0, args);
+          stage_store(to, lane, &maps.o[p.mat], col, row0, p);
         }
       } else if constexpr (EPI == DENSE_GATED) {
         // accumulator columns [0, bn / 2) are g, the others u; 64 hidden columns a
@@ -887,7 +898,7 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
             for (int j = 0; j < 4; ++j)
               sts16(wide_at(to, lane, part * 4 + j), pack8<BF>(*reinterpret_cast<float(*)[8]>(&v[8 * j])));
           }
-          stage_store(to, lane, &maps.o[out], col, row0, args);
+          stage_store(to, lane, &maps.o[out], col, row0, p);
         }
       } else {
 #pragma unroll 1
@@ -917,7 +928,7 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            if (row0 < args.rows && col < args.cols)
+            if (row0 < p.rows && col < p.cols)
               for (int out = 0; out < 3; ++out) tma_store_2d(&maps.o[out], to + out * 2048u, col, row0);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
@@ -1288,7 +1299,13 @@ cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream) {
   a.tn = ceil_div(d.cols, (p.pair ? 256 : 128) / (dual ? 2 : 1));
   a.mats = d.mats;
   if (p.pair) {
-    const int tiles = a.tm * a.tn * a.mats, left = tiles % (kNumSMs / 2);
+    if (d.also != nullptr) {
+      a.rows2 = (int)d.also->rows;
+      a.cols2 = (int)d.also->cols;
+      a.tm2 = ceil_div(a.rows2, 256);
+      a.tn2 = ceil_div(a.cols2, 256);
+    }
+    const int tiles = a.tm * a.tn * a.mats + a.tm2 * a.tn2, left = tiles % (kNumSMs / 2);
     const bool cut = left <= kNumSMs / 4;   // a remainder of at most half a wave is cut in two
     a.whole = cut ? tiles - left : tiles;
     a.items = cut ? tiles + left : tiles;
@@ -1315,6 +1332,7 @@ cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream) {
   // the kernels prefetch every map: the unused ones repeat another
   if (n_a < 2) maps.a[1] = maps.a[0];
   if (n_b < 2) maps.b[1] = maps.b[0];
+  maps.b[2] = maps.b[0];
   if (p.pair) {   // the pair kernel reads its other inputs and stores its outputs with TMA
     const int width = d.epi == DENSE_GRAD ? 32 : 64;
     const uint16_t* r[2] = {d.epi == DENSE_GRAD ? d.g : d.residual, d.epi == DENSE_GRAD ? d.u : nullptr};
@@ -1328,6 +1346,13 @@ cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream) {
         maps.r[i] = maps.o[0];
       else if (!map16(&maps.r[i], r[i], d.cols, d.rows, d.epi == DENSE_GRAD ? d.cols : d.ldr, 32, width))
         return cudaErrorInvalidValue;
+    if (const DenseGemm* e = d.also; e != nullptr) {
+      if (!d.a_mn || !e->a_mn || d.b_k || e->b_k || d.K != e->K) return cudaErrorInvalidValue;
+      if (!map16(&maps.a[1], e->a[0], e->rows, e->K, e->lda, kSlab) ||
+          !map16(&maps.b[2], e->b[0], e->cols, e->K, e->ldb, kSlab) ||
+          !map16(&maps.o[2], e->o[0], e->cols, e->rows, e->ldo, 32))
+        return cudaErrorInvalidValue;
+    }
   }
   return d.bf16 ? launch_typed<true>(d, p, maps, a, stream) : launch_typed<false>(d, p, maps, a, stream);
 }

@@ -37,6 +37,9 @@ struct DenseGemm {
   const uint16_t *g = nullptr, *u = nullptr;   // DENSE_GRAD, rows x cols, contiguous
   uint16_t* o[3] = {};
   int64_t ldo = 0;
+  // another product of the same depth with nothing in its epilogue, in the same
+  // launch (both with a_mn, neither with b_k)
+  const DenseGemm* also = nullptr;
 };
 
 cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream);
