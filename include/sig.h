@@ -19,7 +19,8 @@
  *
  * Conventions shared by every entry point
  *   - Every pointer named WT, x, X, y, Y, h_out, mask_bits, idx, nnz, ws,
- *     down_norms, norms, packed, X_masked is a DEVICE pointer.  The caller owns
+ *     down_norms, norms, packed, X_masked, bias, residual, g, u, or a gradient
+ *     (d...) of one of them is a DEVICE pointer.  The caller owns
  *     every buffer; the library allocates nothing, keeps no pointer after the
  *     call returns, and never synchronises the device.
  *   - fp16 buffers hold IEEE binary16 bit patterns (uint16_t).
@@ -549,7 +550,8 @@ SIG_API int gated_mlp_sparse_noalloc(const uint16_t* x, const uint16_t* WgT, con
  *   residual [rows x N], row r at residual + r ldr; nullable (ldr is ignored then).
  *   Y        [rows x N] out, row r at Y + r ldy; entries between rows are left
  *            as they were.  Y may be the residual buffer itself (same pointer
- *            and stride); it must not overlap anything else that is read.
+ *            and stride, else SIG_ERR_ARG); it must not overlap anything else
+ *            that is read (Y == X: SIG_ERR_ARG).
  * 0 <= rows <= 2^24 (0: nothing is read or written), 1 <= K <= 2^20,
  * 8 <= N <= 2^20, N % 8 == 0; each stride at least its row's length, a multiple
  * of 8 and at most 2^30; every pointer 16-byte aligned.
@@ -580,8 +582,8 @@ SIG_API int linear_act(const uint16_t* X, int64_t rows, int64_t K, int64_t ldx,
  *        256-byte aligned, for h; it needs no initialisation and holds nothing
  *        from call to call.  NULL when h_out is given.
  * 0 <= rows <= 2^24, 8 <= d_model, d_ff <= 2^20, both multiples of 8; pointers
- * and strides as linear_act.  Outputs must not overlap inputs or each other
- * (but Y the residual).
+ * and strides as linear_act.  Outputs must not overlap inputs or each other,
+ * but Y may be the residual (same stride, else SIG_ERR_ARG) or X.
  * Errors: as linear_act, SIG_ERR_NULL also for one of g_out and u_out alone,
  *         SIG_ERR_WORKSPACE.
  */
@@ -609,7 +611,10 @@ SIG_API int gated_mlp(const uint16_t* X, int64_t rows, int64_t ldx, const uint16
  *   ws   sig_workspace_bytes(SIG_OP_GATED_BACKWARD, d_model, d_ff, rows) bytes,
  *        256-byte aligned, for dg, du and h; needs no initialisation and holds
  *        nothing from call to call (NULL for rows == 0).
- * Limits, alignment and errors as gated_mlp.  Bit-identical from run to run.
+ * Outputs must not overlap inputs or each other; dX may be dY or X where no
+ * weight gradient is wanted (with one it is SIG_ERR_ARG: they are read after dX
+ * is written).  Limits, alignment and errors as gated_mlp.  Bit-identical from
+ * run to run.
  */
 SIG_API int gated_mlp_backward(const uint16_t* dY, int64_t lddy, const uint16_t* X, int64_t ldx,
                                int64_t rows, const uint16_t* g, const uint16_t* u,

@@ -485,6 +485,8 @@ int linear_act(const uint16_t* X, int64_t rows, int64_t K, int64_t ldx, const ui
       {check_rows(X, ldx, K), check_rows(residual, ldr, N), check_rows(Y, ldy, N)});
   if (bad != SIG_OK) return bad;
   if (!aligned16(WT) || !aligned16(bias)) return SIG_ERR_ALIGN;
+  // other tiles still read X while Y is written; a residual in Y's place has Y's rows
+  if (Y == X || (Y == residual && ldy != ldr)) return SIG_ERR_ARG;
   DenseGemm d;
   d.bf16 = dtype == SIG_BF16;
   d.rows = rows; d.cols = N; d.K = K;
@@ -513,6 +515,7 @@ int gated_mlp(const uint16_t* X, int64_t rows, int64_t ldx, const uint16_t* WgT,
   if (!aligned16(WgT) || !aligned16(WuT) || !aligned16(WdT) || !aligned16(h_out) ||
       !aligned16(g_out) || !aligned16(u_out))
     return SIG_ERR_ALIGN;
+  if (Y == residual && ldy != ldr) return SIG_ERR_ARG;
   if (h_out == nullptr) {
     if (ws == nullptr || ws_bytes < hidden_bytes(rows, d_ff)) return SIG_ERR_WORKSPACE;
     if (!aligned256(ws)) return SIG_ERR_ALIGN;
@@ -567,6 +570,8 @@ int gated_mlp_backward(const uint16_t* dY, int64_t lddy, const uint16_t* X, int6
   if (bad != SIG_OK) return bad;
   if (!aligned16(g) || !aligned16(u) || !aligned16(WgT) || !aligned16(WuT) || !aligned16(WdT))
     return SIG_ERR_ALIGN;
+  // the weight gradients read dY and X after dX is written
+  if ((dWgT != nullptr || dWdT != nullptr) && dX != nullptr && (dX == dY || dX == X)) return SIG_ERR_ARG;
   const size_t hb = hidden_bytes(rows, d_ff);
   if (ws == nullptr || ws_bytes < 3 * hb) return SIG_ERR_WORKSPACE;
   if (!aligned256(ws)) return SIG_ERR_ALIGN;

@@ -658,7 +658,6 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   volatile int* abort_flag = &sm.abort_flag;
-  pdl_trigger();
 
   if (warp == 9 && lane < 10)
     prefetch_map(lane < 2   ? &maps.a[lane]
@@ -681,6 +680,8 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
+  // All of tensor memory, at once: nothing else that uses it fits beside this
+  // CTA's shared memory (see dense_few_kernel).
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(&sm.tmem_base)),
@@ -689,10 +690,11 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
   __syncwarp();
-  cluster_sync();
+  cluster_sync();   // both CTAs' barriers exist before anything targets them
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = sm.tmem_base;
   pdl_wait();
+  pdl_trigger();
   const long long limit = wait_limit();
 
   int issued = 0;   // stages whose copies this CTA's producer has issued
@@ -1011,7 +1013,6 @@ dense_few_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__
   const int kb_lo = (int)((int64_t)args.kbt * rank / ranks);
   const int steps = (int)((int64_t)args.kbt * (rank + 1) / ranks) - kb_lo;
   volatile int* abort_flag = &sm.abort_flag;
-  pdl_trigger();
 
   if (warp == 2 && lane < 4) prefetch_map(lane < 2 ? &maps.a[lane] : &maps.b[lane - 2]);
   if (tid == 0) {
@@ -1025,16 +1026,7 @@ dense_few_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
-  if (warp == 0) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(&sm.tmem_base)),
-                 "r"(fs.tmem)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  }
   __syncthreads();
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-  const uint32_t tmem = sm.tmem_base;
   // every CTA of the cluster runs once this barrier is passed (waited for
   // before the first access to another CTA's shared memory)
   if (ranks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
@@ -1062,6 +1054,17 @@ dense_few_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__
       if (++s == S) { s = 0; ph ^= 1u; }
     }
   } else if (warp == 1) {   // ---- MMA issuer: the warp loops, one lane issues ----
+    // Tensor memory only now, with the launch before this one complete, and only
+    // then may the next one start: CTAs of several launches fit an SM, and one
+    // that waits for another must not hold what the other may still ask for.
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sm.tmem_base)),
+                 "r"(fs.tmem)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("barrier.cta.sync.aligned 1, 32;" ::: "memory");   // this warp: the address is visible
+    const uint32_t tmem = *(volatile uint32_t*)&sm.tmem_base;
+    pdl_trigger();
     const uint32_t idesc = dense_idesc(kTile, fs.tn, BF, !B_K, true);
     const uint32_t w_low = slab_low<!B_K>(smem_u32(ring)), x_low = slab_low<false>(smem_u32(ring) + kOperand);
     int s = 0, used = 0;
@@ -1090,6 +1093,7 @@ dense_few_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__
   // one verdict for the CTA: the tensor-memory loads below need whole warps
   const bool ok = __syncthreads_and(acc_done && !*abort_flag) != 0;
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = *(volatile uint32_t*)&sm.tmem_base;
   const int valid = min(fs.tn, args.rows - t0);    // tokens of this tile
   const int own = (valid + ranks - 1) / ranks;     // rank r joins tokens [r own, (r + 1) own)
 
@@ -1110,7 +1114,7 @@ dense_few_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__
     for (int i = sm.consumed; i < issued; ++i)
       wait_drain(smem_u32(&sm.full[i % S]), (uint32_t)(i / S) & 1u);
   __syncthreads();
-  if (warp == 0)
+  if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(fs.tmem)
                  : "memory");
 }

@@ -11,6 +11,7 @@ from tests.conftest import ROOT, load_builder
 OK, NULL, SHAPE, ALIGN, WORKSPACE, CUDA, TIMEOUT, ARG = range(8)
 P = 1 << 40                # an aligned, never dereferenced "device" address
 ODD = P + 2
+OUT = P + (1 << 32)        # another, for outputs
 F16, BF16 = 0, 1
 BIG = 1 << 60
 
@@ -27,7 +28,7 @@ def lib():
 
 
 def linear(lib, **kw):
-    a = dict(X=P, rows=4, K=64, ldx=64, WT=P, N=64, bias=None, act=0, residual=None, ldr=0, Y=P, ldy=64,
+    a = dict(X=P, rows=4, K=64, ldx=64, WT=P, N=64, bias=None, act=0, residual=None, ldr=0, Y=OUT, ldy=64,
              dtype=F16)
     a.update(kw)
     return lib.linear_act(*a.values(), None)
@@ -35,14 +36,14 @@ def linear(lib, **kw):
 
 def gated(lib, **kw):
     a = dict(X=P, rows=4, ldx=64, WgT=P, WuT=P, WdT=P, d_model=64, d_ff=128, act=4, residual=None, ldr=0,
-             Y=P, ldy=64, h_out=None, g_out=None, u_out=None, dtype=F16, ws=P, ws_bytes=BIG)
+             Y=OUT, ldy=64, h_out=None, g_out=None, u_out=None, dtype=F16, ws=P, ws_bytes=BIG)
     a.update(kw)
     return lib.gated_mlp(*a.values(), None)
 
 
 def backward(lib, **kw):
     a = dict(dY=P, lddy=64, X=P, ldx=64, rows=4, g=P, u=P, WgT=P, WuT=P, WdT=P, d_model=64, d_ff=128,
-             act=4, dX=P, lddx=64, dWgT=P, dWuT=P, dWdT=P, dtype=F16, ws=P, ws_bytes=BIG)
+             act=4, dX=OUT, lddx=64, dWgT=P, dWuT=P, dWdT=P, dtype=F16, ws=P, ws_bytes=BIG)
     a.update(kw)
     return lib.gated_mlp_backward(*a.values(), None)
 
@@ -63,6 +64,10 @@ def test_linear_act_validation(lib):
         assert linear(lib, **kw) == ARG, kw
     # an empty block touches no pointer
     assert linear(lib, rows=0, X=None, WT=None, Y=None) == OK
+    # outputs in the place of what is still read
+    Q = P + (1 << 30)
+    assert linear(lib, X=Q, Y=Q) == ARG
+    assert linear(lib, residual=Q, ldr=72, Y=Q, X=P) == ARG
 
 
 def test_gated_mlp_validation(lib):
@@ -81,6 +86,7 @@ def test_gated_mlp_validation(lib):
     assert need == 4 * 128 * 2
     assert gated(lib, ws=None) == WORKSPACE and gated(lib, ws_bytes=need - 1) == WORKSPACE
     assert gated(lib, rows=0, X=None, Y=None, ws=None, ws_bytes=0) == OK
+    assert gated(lib, residual=OUT, ldr=72) == ARG                  # Y with the residual's rows elsewhere
 
 
 def test_gated_mlp_backward_validation(lib):
@@ -95,6 +101,9 @@ def test_gated_mlp_backward_validation(lib):
     for kw in (dict(rows=-1), dict(d_model=20), dict(d_ff=4), dict(lddy=8), dict(ldx=8), dict(lddx=8)):
         assert backward(lib, **kw) == SHAPE, kw
     assert backward(lib, dtype=3) == ARG and backward(lib, act=5) == ARG
+    Q = P + (1 << 30)
+    for kw in (dict(dX=Q, dY=Q), dict(dX=Q, X=Q), dict(dX=Q, X=Q, dWdT=None), dict(dX=Q, dY=Q, dWgT=None, dWuT=None)):
+        assert backward(lib, **kw) == ARG, kw
     need = lib.sig_workspace_bytes(11, 64, 128, 4)
     assert need == 3 * 4 * 128 * 2
     assert backward(lib, ws=None) == WORKSPACE and backward(lib, ws_bytes=need - 1) == WORKSPACE

@@ -336,6 +336,128 @@ def test_gradients_against_differences(sig):
             assert abs((got[i].double() * d).sum().item() - diff) <= ((tol + lim) * d.abs()).sum().item(), (act, i)
 
 
+@pytest.mark.parametrize("rows", [5, 90, 300])
+def test_nothing_between_the_rows_is_read(sig, rows):
+    """NaN in the gaps of strided inputs, behind the last row and around the
+    weights reaches no output."""
+    import torch
+    K, N = 100, 264
+
+    def gapped(seed, r, c, ld, scale=1.0):
+        buf = torch.full((r + 2, ld), float("nan"), dtype=torch.float16, device="cuda")
+        buf[1:r + 1, 8:8 + c] = normal(seed, r, c, scale=scale)
+        return buf[1:r + 1, 8:8 + c]
+
+    X, R = gapped(100, rows, K, 136), gapped(101, rows, N, 304)
+    flat = torch.full((K * N + 128,), float("nan"), dtype=torch.float16, device="cuda")
+    flat[64:64 + K * N] = normal(102, K, N, scale=0.1).reshape(-1)
+    W = flat[64:64 + K * N].view(K, N)
+    y, e = product(X, W)
+    y = y + R.double()
+    within(sig.linear_act(X, W, residual=R), y, rounding(y, e + U * y.abs(), "fp16"), "gaps")
+    m, f = 104, 136
+    X, dY = gapped(103, rows, m, 120), gapped(104, rows, m, 144)
+    g, u = normal(105, rows, f), normal(106, rows, f)
+    Wg, Wu, Wd = normal(107, m, f, scale=0.1), normal(108, m, f, scale=0.1), normal(109, f, m, scale=0.1)
+    got = sig.gated_mlp_backward(dY, X, g, u, Wg, Wu, Wd)
+    want = sig.gated_mlp_backward(dY.contiguous(), X.contiguous(), g, u, Wg, Wu, Wd)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and all(bool(v.isfinite().all()) for v in got)
+
+
+@pytest.mark.parametrize("rows", [3, 200])
+def test_outputs_in_the_place_of_inputs(sig, rows):
+    """The places that the documentation allows give the same bits; the others are refused."""
+    import torch
+    args = backward_inputs(rows, 264, 520, "fp16", seed=110)
+    dY, X, g, u, Wg, Wu, Wd = args
+    want = sig.gated_mlp(X, Wg, Wu, Wd, residual=X)
+    S = X.clone()
+    sig.gated_mlp(S, Wg, Wu, Wd, residual=S, Y=S)
+    assert torch.equal(S, want)
+    dX = sig.gated_mlp_backward(*args, want_weights=False)[0]
+    for i in (0, 1):
+        moved = [t.clone() for t in args]
+        sig.gated_mlp_backward(*moved, dX=moved[i], want_weights=False)
+        assert torch.equal(moved[i], dX)
+        with pytest.raises(sig.SigError):
+            sig.gated_mlp_backward(*moved, dX=moved[i])
+    sq = normal(117, 264, 264)
+    with pytest.raises(sig.SigError):
+        sig.linear_act(X, sq, Y=X)
+
+
+def test_two_threads(sig):
+    """Two host threads, each on its own stream."""
+    import threading
+    import torch
+    sets = [backward_inputs(100 + 200 * i, 264, 520, "fp16", seed=150 + 10 * i) for i in range(2)]
+    want = [(sig.gated_mlp(s[1], *s[4:]), *sig.gated_mlp_backward(*s)) for s in sets]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                got = (sig.gated_mlp(sets[i][1], *sets[i][4:]), *sig.gated_mlp_backward(*sets[i]))
+            torch.cuda.current_stream().synchronize()
+            wrong.extend(k for k, (a, b) in enumerate(zip(got, want[i])) if not torch.equal(a, b))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert wrong == []
+
+
+def test_the_first_call_may_be_captured():
+    """In a process that has called nothing of the library, the first calls go
+    straight into a graph; its replay gives the eager bits."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, sparse_input_gemv_threshold_b200 as sig
+X = torch.randn(300, 256, device='cuda').half(); W = torch.randn(256, 512, device='cuda').half() * 0.1
+D = torch.randn(512, 256, device='cuda').half() * 0.1
+s = torch.cuda.Stream(); g = torch.cuda.CUDAGraph()
+torch.cuda.synchronize()
+with torch.cuda.graph(g, stream=s):
+    a = sig.gated_mlp(X, W, W, D); b = sig.gated_mlp(X[:3], W, W, D)
+g.replay(); torch.cuda.synchronize()
+assert torch.equal(a, sig.gated_mlp(X, W, W, D)) and torch.equal(b, sig.gated_mlp(X[:3], W, W, D))
+assert sig.take_device_error() == 0 and bool(a.isfinite().all())
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_beside_the_other_tensor_core_kernels(sig):
+    """Blocks of tokens on one stream and the N:M GEMMs on another, and in turn on
+    one: kernels that ask for tensor memory side by side."""
+    import torch
+    import oracle
+    import workloads
+    WT, Xn = workloads.nm_tokens(7, rows=512, d=512, d_out=512)
+    dW, dXn = torch.from_numpy(WT).cuda(), torch.from_numpy(Xn).cuda()
+    Y64, B = oracle.nm_gemm(Xn, WT, oracle.nm_mask(Xn, 2, 4))
+    X, W = normal(160, 40, 512), normal(161, 512, 1096, scale=0.05)
+    Xb = normal(162, 700, 512)
+    want = sig.linear_act(X, W), sig.linear_act(Xb, W)
+    wantn = sig.nm_act_gemm(dXn, dW, 2, 4)
+    assert np.all(np.abs(wantn.cpu().numpy().astype(np.float64) - Y64) <= 2e-3 * B + 2.0 ** -24)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(30):
+        a = sig.linear_act(X, W, stream=s1), sig.linear_act(Xb, W, stream=s1)
+        n2 = sig.nm_act_gemm(dXn, dW, 2, 4, stream=s2)
+        n1 = sig.nm_act_gemm(dXn, dW, 2, 4, stream=s1)
+        b = sig.linear_act(X, W, stream=s2)
+    torch.cuda.synchronize()
+    assert torch.equal(a[0], want[0]) and torch.equal(a[1], want[1]) and torch.equal(b, want[0])
+    assert torch.equal(n1, wantn) and torch.equal(n2, wantn)
+
+
 def test_empty_blocks(sig):
     import torch
     X, W = normal(50, 0, 64), normal(51, 64, 32)
