@@ -2,15 +2,22 @@
 // gate and up projections of a gated MLP with the activation and the product
 // of the two in the epilogue, and the products of its backward pass.
 //
-//   dense_pair_kernel  persistent: CTA pairs walk tiles of 256 tokens x 128 or
-//                      256 columns with two accumulators in tensor memory, so
-//                      the epilogue of a tile runs beside the mainloop of the next.
+//   dense_pair_kernel  persistent: CTA pairs walk tiles of 256 tokens x 256 (or
+//                      128) columns with two accumulators in tensor memory, so
+//                      the epilogue of a tile runs beside the mainloop of the
+//                      next.  Bound by the tensor cores at the power limit:
+//                      4096 x 4096 x 4096 fp16 in 91-94 us on B200 (1.5 PFLOP/s,
+//                      0.9 of the measured burst rate; 77 % of the launch with
+//                      the tensor pipe active at 1.55 GHz).
 //   dense_few_kernel   few tokens, bound by reading the weight: the weight is the
 //                      MMA's M operand (128 of its columns, one a tensor-memory
 //                      lane) and the tokens its N operand; one tile per cluster,
 //                      whose CTAs each take a part of K and join their float32
 //                      sums through distributed shared memory in a fixed order:
 //                      no workspace, no atomics, the same bits in every run.
+//                      16 tokens 4096 -> 11008: 17.5 us, 5.2 TB/s of weight
+//                      (0.79 of the measured copy rate); 1 token 4096 -> 4096
+//                      8.5 us, of which 5.1 are the weight at that rate.
 #include "common.cuh"
 #include "dense.h"
 #include "internal.h"
@@ -116,7 +123,8 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
 
 // Hands an accumulator back: the tensor-memory loads are done and fenced, and no
 // other memory is passed on, so the arrive needs no release (whose wait for the
-// warp's earlier stores costs 15 us of 59 at 4096 x 16 x 22016, all epilogue).
+// warp's earlier stores made 59 us of the 44 that 22016 x 4096 outputs of depth 16
+// take otherwise).
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
@@ -270,8 +278,8 @@ constexpr float kGeluC = 0.79788456080286536f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
 // 1 / (1 + exp(-v)) with the hardware's exponential and reciprocal: a relative
-// error of about (3 + 1.2 |v|) 2^-23, and 0 where exp(-v) passes 2^126 (the IEEE
-// division took 16 us of 42 at 2048 x 1024 x 2816 with SiLU and its slope).
+// error of about (3 + 1.2 |v|) 2^-23, and 0 where exp(-v) passes 2^126 (with
+// the IEEE division 2048 x 1024 -> 2816 took 25.0 us with SiLU, now 15.1).
 __device__ __forceinline__ float logistic(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
 // exp(-z^2 / 2)
@@ -560,7 +568,8 @@ constexpr int kSmemPerCta = 227 * 1024, kSmemPerSm = 228 * 1024;   // a CTA cost
 // accumulator, and in its place what it stores: two of 32 rows x 64 columns, or
 // for DENSE_GRAD two sets of three of 32 x 32, at the price of a ring stage.
 // Lanes reading 16 bytes of 32 different rows straight from global memory
-// instead took 41 of 147 us of the gradient's first product at 2048 x 4096 x 11008.
+// took 31.9 us instead of 27.4 in the gradient's first product, 2048 tokens
+// 1024/2816.
 template <int EPI>
 struct PairCfg {
   static constexpr int kStages = EPI == DENSE_GRAD ? 4 : 5;
@@ -1148,27 +1157,27 @@ struct DensePlan {
 
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
 
-// Which kernel, and how a few-token launch is split.
-//
-// Up to 64 tokens the launch is bound by reading the weight and two CTAs fit an
-// SM.  K is split until there are 128 CTAs, and on while each keeps 16
-// stages and the clusters run at once: measured on B200 with 16 tokens, 4096 -> 4096 9.1 us with 4 parts
-// against 10.0 with 8 and 9.6 with 3; 11008 -> 4096 17.9 with 8 against 18.8
-// with 4; 4096 -> 11008 17.7 with 3 against 20.3 with 1.
-// From 65 to 1024 tokens both kernels are in play, bound by what a stage takes to
-// arrive (about 110 KB/us an SM): the few-token kernel with a few blocks of
-// tokens and K split over the SMs, or the pair kernel with its whole and half
-// tiles.  The estimates below (in us; the constants are those of the measured
-// stages, joins and launches) pick the faster one at 192 tokens: 4096 -> 4096
-// few 15.0 against 19.5 us, 4096 -> 11008 pair 26.6 against 29.8,
-// 1024 -> 2816 pair 8.7 against 8.8.  Beyond 1024 tokens the pair kernel fills
-// the GPU.
 // Clusters of 1 .. 8 CTAs are placed within a GPC, so fewer of the larger ones
 // fit at once: what cudaOccupancyMaxActiveClusters gives for the few-token
 // kernel's shared memory with one and with two CTAs on an SM.
 constexpr int kClusters1[kFewCluster + 1] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
 constexpr int kClusters2[kFewCluster + 1] = {0, 296, 148, 93, 71, 56, 45, 37, 33};
 
+// Which kernel, and how a few-token launch is split.
+//
+// Up to 64 tokens the launch is bound by reading the weight and two CTAs fit an
+// SM.  K is split until there are 128 CTAs, and on while each keeps 16 stages and
+// the clusters run at once.  Measured on B200 with 16 tokens: 4096 -> 4096 9.1 us
+// with 4 parts against 10.0 with 8 and 9.6 with 3; 11008 -> 4096 17.9 with 8
+// against 18.8 with 4; 4096 -> 11008 17.7 with 3 against 20.3 with 1.
+//
+// From 65 to 1024 tokens both kernels are in play, bound by what a stage takes to
+// arrive (about 110 KB/us an SM): the few-token kernel with a few blocks of tokens
+// and K split over the SMs, or the pair kernel with its whole and half tiles.  The
+// estimates below, in us, pick the faster; their constants are those of measured
+// stages, joins and launches.  At 192 tokens: 4096 -> 4096 few 15.0 against pair
+// 19.5 us, 4096 -> 11008 pair 26.6 against few 29.8, 1024 -> 2816 pair 8.7 against
+// few 8.8.  Beyond 1024 tokens the pair kernel fills the GPU.
 DensePlan plan_dense(const DenseGemm& d, int kbt) {
   const DensePlan pair = {true, 0, 0, 0};
   if (d.a_mn || d.rows > 1024) return pair;
@@ -1230,8 +1239,7 @@ cudaError_t launch_cluster(dim3 grid, int threads, int cluster, size_t smem, cud
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, FN, maps, args, shape...);
-  return e != cudaSuccess ? e : cudaPeekAtLastError();
+  return cudaLaunchKernelEx(&cfg, FN, maps, args, shape...);
 }
 
 template <bool A_MN, bool B_K, int EPI, bool BF>
