@@ -371,7 +371,16 @@ __device__ __forceinline__ void epi_gated(float* g, const float* u, int act) {
   });
 }
 
-// dh -> (dg, du, h) over 8 columns
+// dh -> (dg, du, h)
+template <int ACT>
+__device__ __forceinline__ void gate_grad(float dh, float g, float u, float& dg, float& du, float& h) {
+  const float p = act_share<ACT>(g), v = act_value<ACT>(g, p);
+  dg = dh * u * act_slope<ACT>(g, p);
+  du = dh * v;
+  h = v * u;
+}
+
+// the same over 8 columns
 template <bool BF>
 __device__ __forceinline__ void epi_grad8(const float* dh, const uint4& gv, const uint4& uv, int act,
                                           uint4& dg, uint4& du, uint4& h) {
@@ -379,77 +388,82 @@ __device__ __forceinline__ void epi_grad8(const float* dh, const uint4& gv, cons
   unpack8<BF>(g, gv);
   unpack8<BF>(u, uv);
   with_act(act, [&](auto A) {
-    constexpr int ACT = decltype(A)::value;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float p = act_share<ACT>(g[i]), v = act_value<ACT>(g[i], p);
-      a0[i] = dh[i] * u[i] * act_slope<ACT>(g[i], p);
-      a1[i] = dh[i] * v;
-      a2[i] = v * u[i];
-    }
+    for (int i = 0; i < 8; ++i) gate_grad<decltype(A)::value>(dh[i], g[i], u[i], a0[i], a1[i], a2[i]);
   });
   dg = pack8<BF>(a0);
   du = pack8<BF>(a1);
   h = pack8<BF>(a2);
 }
 
-// What the epilogue of 8 columns of a token reads besides the sums: the
-// residual, or g and u.  Loaded ahead of the sums.
+// What the few-token epilogue of 4 columns of a token reads besides the sums:
+// the residual, or g and u.  Loaded ahead of the sums.
 struct Extra {
-  uint4 x, y;
+  uint2 x, y;
 };
 
 template <int EPI>
 __device__ __forceinline__ Extra load_extra(const DenseArgs& a, int row, int col) {
-  Extra e = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-  if (row >= a.rows || col >= a.cols) return e;
+  Extra e = {make_uint2(0, 0), make_uint2(0, 0)};
   if constexpr (EPI == DENSE_LINEAR) {
     if (a.residual != nullptr)   // a plain load: Y may be the residual buffer itself
-      e.x = *reinterpret_cast<const uint4*>(a.residual + (int64_t)row * a.ldr + col);
+      e.x = *reinterpret_cast<const uint2*>(a.residual + (int64_t)row * a.ldr + col);
   } else if constexpr (EPI == DENSE_GRAD) {
     const int64_t at = (int64_t)row * a.cols + col;
-    e.x = ld16(a.g + at);
-    e.y = ld16(a.u + at);
+    e.x = __ldg(reinterpret_cast<const uint2*>(a.g + at));
+    e.y = __ldg(reinterpret_cast<const uint2*>(a.u + at));
   }
   return e;
 }
 
-__device__ __forceinline__ void store16(uint16_t* p, const uint4& v) { *reinterpret_cast<uint4*>(p) = v; }
+template <bool BF>
+__device__ __forceinline__ float4 unpack4(const uint2& v) {
+  const float2 a = unpack2<BF>(v.x), b = unpack2<BF>(v.y);
+  return make_float4(a.x, a.y, b.x, b.y);
+}
 
-// The outputs of 8 columns of a token from its float32 sums v (DENSE_GATED: g
-// in v and u in w).
-template <int EPI, bool BF>
-__device__ __forceinline__ void finish8(float (&v)[8], const float (&w)[8], const Extra& e,
-                                        const DenseArgs& a, int mat, int row, int col) {
-  const int64_t at = (int64_t)row * a.ldo + col;
+template <bool BF>
+__device__ __forceinline__ uint2 pack4(const float4& v) {
+  return make_uint2(pack2<BF>(v.x, v.y), pack2<BF>(v.z, v.w));
+}
+
+__device__ __forceinline__ float4 add4(const float4& a, const float4& b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+template <int ACT>
+__device__ __forceinline__ float4 act4(const float4& z) {
+  return make_float4(act_value<ACT>(z.x, act_share<ACT>(z.x)), act_value<ACT>(z.y, act_share<ACT>(z.y)),
+                     act_value<ACT>(z.z, act_share<ACT>(z.z)), act_value<ACT>(z.w, act_share<ACT>(z.w)));
+}
+
+// The outputs of 4 columns of a token from its float32 sums v (DENSE_GATED: g
+// in v and u in w, which are outputs 1 and 2).
+template <int EPI, bool BF, int ACT>
+__device__ __forceinline__ void finish4(const float4& v, const float4& w, const float4& bias, const Extra& e,
+                                        uint2& o0, uint2& o1, uint2& o2) {
   if constexpr (EPI == DENSE_LINEAR) {
-    epi_bias_act<BF, 1>(v, a, col);
-    if (a.residual != nullptr) {
-      float r[8];
-      unpack8<BF>(r, e.x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += r[i];
-    }
-    store16(a.o[mat] + at, pack8<BF>(v));
+    o0 = pack4<BF>(add4(act4<ACT>(add4(v, bias)), unpack4<BF>(e.x)));
   } else if constexpr (EPI == DENSE_GATED) {
-    if (a.outs == 3) {
-      store16(a.o[1] + at, pack8<BF>(v));
-      store16(a.o[2] + at, pack8<BF>(w));
-    }
-    epi_gated<8>(v, w, a.act);
-    store16(a.o[0] + at, pack8<BF>(v));
+    const float4 h = act4<ACT>(v);
+    o0 = pack4<BF>(make_float4(h.x * w.x, h.y * w.y, h.z * w.z, h.w * w.w));
+    o1 = pack4<BF>(v);
+    o2 = pack4<BF>(w);
   } else {
-    uint4 dg, du, h;
-    epi_grad8<BF>(v, e.x, e.y, a.act, dg, du, h);
-    store16(a.o[0] + at, dg);
-    store16(a.o[1] + at, du);
-    store16(a.o[2] + at, h);
+    const float4 g = unpack4<BF>(e.x), u = unpack4<BF>(e.y);
+    float4 dg, du, h;
+    gate_grad<ACT>(v.x, g.x, u.x, dg.x, du.x, h.x);
+    gate_grad<ACT>(v.y, g.y, u.y, dg.y, du.y, h.y);
+    gate_grad<ACT>(v.z, g.z, u.z, dg.z, du.z, h.z);
+    gate_grad<ACT>(v.w, g.w, u.w, dg.w, du.w, h.w);
+    o0 = pack4<BF>(dg);
+    o1 = pack4<BF>(du);
+    o2 = pack4<BF>(h);
   }
 }
 
-// 16 tensor-memory columns (tokens) of this warp's 32 lanes
-__device__ __forceinline__ void tmem_ld16(float (&v)[16], uint32_t addr) {
-  uint32_t r[16];
+// The same for 16 columns (tokens)
+__device__ __forceinline__ void tmem_start16(uint32_t (&r)[16], uint32_t addr) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -457,74 +471,147 @@ __device__ __forceinline__ void tmem_ld16(float (&v)[16], uint32_t addr) {
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]),
+                 "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void sts_b32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ float4 lds_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr));
+  return v;
 }
 
 // The join of `parts` CTAs that split K.  Part j joins tokens [j own, (j + 1)
 // own) of the tile.  join_send: eight warps send this CTA's sums of every
 // token to the part that joins it, at [part][token - j own][128 columns] of its
-// buffer; `cta(j)` is part j's rank in the cluster.  A warp's 32 lanes write
-// 128 contiguous bytes, the two warps of a lane quarter take groups of 16
-// tokens in turn.
-template <typename F>
+// buffer, beginning with the part after this one so that the parts do not all
+// send to the same.  A warp's 32 lanes write 128 contiguous bytes, the two
+// warps of a lane quarter take groups of 16 tokens in turn.  One lane a token
+// works out where it goes, so that the stores follow one another without a
+// branch: with the owner found token by token in every lane they took 4 us at
+// 256 tokens, now 1.3.
 __device__ __forceinline__ void join_send(uint32_t buf, uint32_t acc, int warp, int lane, int valid,
-                                          int own, int part, F&& cta) {
+                                          int own, int part) {
   const int q = warp & 3;
-  const uint32_t base = buf + (uint32_t)((part * own * 128 + q * 32 + lane) * 4);
+  const uint32_t at = (uint32_t)((q * 32 + lane) * 4);
+  const int groups = (valid + 15) / 16, turn = (part + 1) * own / 16 % groups;
 #pragma unroll 1
-  for (int c = (warp >> 2) * 16; c < valid; c += 32) {
-    float v[16];
-    tmem_ld16(v, acc + ((uint32_t)(q * 32) << 16) + (uint32_t)c);
-    int owner = c / own, slot = c - owner * own;
-    uint32_t to = map_to_rank(base, cta(owner)) + (uint32_t)slot * 512u;
+  for (int g = warp >> 2; g < groups; g += 2) {
+    const int c = (g + turn < groups ? g + turn : g + turn - groups) * 16;
+    uint32_t r[16];
+    tmem_start16(r, acc + ((uint32_t)(q * 32) << 16) + (uint32_t)c);
+    const int token = min(c + (lane & 15), valid - 1), owner = token / own;
+    const uint32_t to = map_to_rank(buf, (uint32_t)owner) + (uint32_t)((part * own + token - owner * own) * 512);
+    tmem_wait16(r);
+    if (c >= part * own && c + 16 <= (part + 1) * own && c + 16 <= valid) {   // all of them stay here
+      const uint32_t dst = buf + (uint32_t)(c * 512) + at;
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (c + i < valid) {
-        st_cluster_f32(to, v[i]);
-        to += 512u;
-        if (++slot == own && c + i + 1 < valid) {
-          slot = 0;
-          to = map_to_rank(base, cta(++owner));
-        }
+      for (int i = 0; i < 16; ++i) sts_b32(dst + i * 512u, r[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t dst = __shfl_sync(kFull, to, i) + at;
+        if (c + i < valid) st_cluster(dst, r[i]);
       }
+    }
   }
 }
 
-// Adds the parts in order and finishes the tokens of `part`; 256 threads.
-// n0 is the CTA's first output column, t0 the tile's first token.
+// The joining side: adds the parts in order and finishes this CTA's `mine`
+// tokens (the tile's from `first`), 4 columns a lane, so that a warp reads a
+// token's 512 bytes and writes its 256 in one piece each, and keeps the bias in
+// registers.  kJoin tokens are under way in a warp, without a branch between
+// them; what the first of them read from memory is asked for in the
+// constructor, before the sums are there.
+constexpr int kJoin = 4;
+
 template <int EPI, bool BF>
-__device__ __forceinline__ void join_finish(const uint8_t* buf, const DenseArgs& args, int mat, int n0,
-                                            int t0, int valid, int own, int part, int parts) {
-  constexpr int kChunks = EPI == DENSE_GATED ? 8 : 16;   // 8-column chunks of a token
-  const int mine = min(own, valid - part * own);         // may be negative: nothing to join
-  for (int i = threadIdx.x; i < mine * kChunks; i += 256) {
-    const int slot = i / kChunks, ch = i % kChunks;
-    const int row = t0 + part * own + slot, col = n0 + ch * 8;
-    if (col >= args.cols) continue;
-    const Extra e = load_extra<EPI>(args, row, col);
-    auto gather = [&](float (&v)[8], int first) {
+struct Join {
+  static constexpr int kLanes = EPI == DENSE_GATED ? 16 : 32;   // lanes of a token
+  static constexpr int kStep = 256 / kLanes;                    // tokens that the CTA takes at once
+  const DenseArgs& args;
+  int mat, row0, col, mine, slot, ch;
+  float4 bias;
+  Extra e[kJoin];
+
+  __device__ __forceinline__ Join(const DenseArgs& a, int m, int n0, int first, int tokens)
+      : args(a), mat(m), row0(first), mine(tokens), bias(make_float4(0.f, 0.f, 0.f, 0.f)) {
+    slot = (int)threadIdx.x / kLanes;
+    ch = (int)threadIdx.x % kLanes * 4;
+    col = n0 + ch;
+    if (col >= a.cols) mine = 0;
+    if (EPI == DENSE_LINEAR && a.bias != nullptr && slot < mine)
+      bias = unpack4<BF>(__ldg(reinterpret_cast<const uint2*>(a.bias + col)));
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = 0.f;
-      for (int src = 0; src < parts; ++src) {
-        const float4* f =
-            reinterpret_cast<const float4*>(buf + (size_t)((src * own + slot) * 128 + first) * 4);
-        const float4 a = f[0], b = f[1];
-        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
-        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
-      }
-    };
-    float v[8], w[8] = {};
-    gather(v, ch * 8);
-    if constexpr (EPI == DENSE_GATED) gather(w, 64 + ch * 8);
-    finish8<EPI, BF>(v, w, e, args, mat, row, col);
+    for (int t = 0; t < kJoin; ++t) e[t] = {make_uint2(0, 0), make_uint2(0, 0)};
+    fetch(slot);
   }
-}
+
+  __device__ __forceinline__ void fetch(int s) {
+    if (EPI == DENSE_GRAD || (EPI == DENSE_LINEAR && args.residual != nullptr))
+#pragma unroll
+      for (int t = 0; t < kJoin; ++t)
+        if (s + t * kStep < mine) e[t] = load_extra<EPI>(args, row0 + s + t * kStep, col);
+  }
+
+  __device__ __forceinline__ void finish(uint32_t buf, int own, int parts) {
+    if (slot >= mine) return;
+    with_act(args.act, [&](auto A) {
+#pragma unroll 1
+      for (int s = slot; s < mine; s += kJoin * kStep) {
+        uint32_t f[kJoin];
+        float4 v[kJoin], w[kJoin];
+#pragma unroll
+        for (int t = 0; t < kJoin; ++t) {
+          f[t] = buf + (uint32_t)((min(s + t * kStep, mine - 1) * 128 + ch) * 4);
+          v[t] = w[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll 1
+        for (int src = 0; src < parts; ++src)
+#pragma unroll
+          for (int t = 0; t < kJoin; ++t) {
+            v[t] = add4(v[t], lds_f32x4(f[t]));
+            if constexpr (EPI == DENSE_GATED) w[t] = add4(w[t], lds_f32x4(f[t] + 256u));
+            f[t] += (uint32_t)own * 512u;
+          }
+        uint2 o[3][kJoin];
+#pragma unroll
+        for (int t = 0; t < kJoin; ++t)
+          finish4<EPI, BF, decltype(A)::value>(v[t], w[t], bias, e[t], o[0][t], o[1][t], o[2][t]);
+        const int64_t at = (int64_t)(row0 + s) * args.ldo + col, step = (int64_t)kStep * args.ldo;
+        store(args.o[EPI == DENSE_LINEAR ? mat : 0] + at, step, s, o[0]);
+        if (EPI == DENSE_GRAD || (EPI == DENSE_GATED && args.outs == 3)) {
+          store(args.o[1] + at, step, s, o[1]);
+          store(args.o[2] + at, step, s, o[2]);
+        }
+        fetch(s + kJoin * kStep);
+      }
+    });
+  }
+
+  __device__ __forceinline__ void store(uint16_t* to, int64_t step, int s, const uint2 (&o)[kJoin]) {
+#pragma unroll
+    for (int t = 0; t < kJoin; ++t)
+      if (s + t * kStep < mine) *reinterpret_cast<uint2*>(to + t * step) = o[t];
+  }
+};
 
 // The weight's boxes of K stage kb for a CTA's 128 accumulator lanes from
 // output column n0: each(map, coordinates, byte offset in the operand).
@@ -1098,25 +1185,25 @@ dense_few_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__
     __syncwarp();
   }
 
+  const int valid = min(fs.tn, args.rows - t0);    // tokens of this tile
+  const int own = (valid + ranks - 1) / ranks;     // rank r joins tokens [r own, (r + 1) own)
+  Join<EPI, BF> last(args, mat, n0, t0 + rank * own, min(own, valid - rank * own));
+
   const bool acc_done = wait_drain(smem_u32(&sm.accum), 0u);
   // one verdict for the CTA: the tensor-memory loads below need whole warps
   const bool ok = __syncthreads_and(acc_done && !*abort_flag) != 0;
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *(volatile uint32_t*)&sm.tmem_base;
-  const int valid = min(fs.tn, args.rows - t0);    // tokens of this tile
-  const int own = (valid + ranks - 1) / ranks;     // rank r joins tokens [r own, (r + 1) own)
-
   if (ranks > 1) {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (fs.join == 0) cluster_sync();   // the ring is free once every CTA's MMAs are done
   }
-  if (ok)
-    join_send(smem_u32(join), tmem, warp, lane, valid, own, rank, [](int j) { return (uint32_t)j; });
+  if (ok) join_send(smem_u32(join), tmem, warp, lane, valid, own, rank);
   if (ranks > 1)
     cluster_sync();
   else
     __syncthreads();
-  if (ok) join_finish<EPI, BF>(join, args, mat, n0, t0, valid, own, rank, ranks);
+  if (ok) last.finish(smem_u32(join), own, ranks);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (tid == 0 && *abort_flag)
@@ -1172,12 +1259,14 @@ constexpr int kClusters2[kFewCluster + 1] = {0, 296, 148, 93, 71, 56, 45, 37, 33
 // against 18.8 with 4; 4096 -> 11008 17.7 with 3 against 20.3 with 1.
 //
 // From 65 to 1024 tokens both kernels are in play, bound by what a stage takes to
-// arrive (about 110 KB/us an SM): the few-token kernel with a few blocks of tokens
-// and K split over the SMs, or the pair kernel with its whole and half tiles.  The
-// estimates below, in us, pick the faster; their constants are those of measured
-// stages, joins and launches.  At 192 tokens: 4096 -> 4096 few 15.0 against pair
-// 19.5 us, 4096 -> 11008 pair 26.6 against few 29.8, 1024 -> 2816 pair 8.7 against
-// few 8.8.  Beyond 1024 tokens the pair kernel fills the GPU.
+// arrive (about 136 KB/us an SM): the few-token kernel with blocks of 64 tokens or
+// more and K split over the SMs, or the pair kernel with its whole and half tiles.
+// The estimates below, in us, pick the faster.  Their constants were fitted to 266
+// shapes of 65 - 1024 tokens, K of 256 - 11008 and 512 - 16384 outputs, each timed
+// with every split that fits: the choice costs 1.0 % over the fastest on average.
+// At 256 tokens: 4096 -> 4096 few 12.7 against pair 20.9 us, 4096 -> 11008 pair 26.2
+// against few 29.5, 1024 -> 1024 few 5.6 against pair 7.7.  Beyond 1024 tokens the
+// pair kernel fills the GPU.
 DensePlan plan_dense(const DenseGemm& d, int kbt) {
   const DensePlan pair = {true, 0, 0, 0};
   if (d.a_mn || d.rows > 1024) return pair;
@@ -1190,13 +1279,13 @@ DensePlan plan_dense(const DenseGemm& d, int kbt) {
   }
   const int tiles = ceil_div(d.rows, 256) * d.mats * ceil_div(d.cols * shrink, 256);
   const int waves = tiles / (kNumSMs / 2), left = tiles % (kNumSMs / 2);
-  double best = 4.5 + kbt * (0.36 * waves + (left == 0 ? 0.0 : left <= kNumSMs / 4 ? 0.22 : 0.33));
+  double best = 3.9 + kbt * (0.32 * waves + (left == 0 ? 0.0 : left <= kNumSMs / 4 ? 0.245 : 0.335));
   DensePlan plan = pair;
-  for (int blocks = ceil_div(d.rows, 256); blocks <= ceil_div(d.rows, 128); ++blocks) {
+  for (int blocks = ceil_div(d.rows, 256); blocks <= ceil_div(d.rows, 64); ++blocks) {
     const int tn = ceil_div(ceil_div(d.rows, blocks), 16) * 16, few = blocks * cols;
     for (int parts = 1; parts <= std::min(kFewCluster, kbt); ++parts) {
-      const double stage = (16.0 + tn / 8.0) / 110.0, join = tn * 0.5 * (parts - 1) / parts / 20.0;
-      const double t = ceil_div(few, kClusters1[parts]) * (5.0 + ceil_div(kbt, parts) * stage) + join;
+      const double stage = (16.0 + tn / 8.0) / 136.0, join = tn * (0.01 + 0.02 * (parts - 1) / parts);
+      const double t = ceil_div(few, kClusters1[parts]) * (2.6 + ceil_div(kbt, parts) * stage + join);
       if (t < best) {
         best = t;
         plan = {false, tn, parts, 1};
@@ -1264,10 +1353,12 @@ cudaError_t launch_few(const DensePlan& p, const DenseMaps& maps, const DenseArg
   // shared memory of a CTA: half of the SM's 228 KB (less 1 KB a CTA), or what one CTA may have
   const int budget = (p.per_sm == 2 ? kSmemPerSm / 2 - 1024 : kSmemPerCta) - extra;
   // The join: tn tokens x 128 columns of float32, rounded up to whole ranks.
-  // Up to 64 tokens it has a place of its own, which saves the cluster barrier
-  // that says that every ring is free; above, it takes the ring's.
+  // Up to 96 tokens it has a place of its own, which saves the cluster barrier
+  // that says that every ring is free (96 x 4096 -> 4096: 10.6 against 11.1 us);
+  // above, the ring would lose too many stages (256 x 4096 -> 4096 in two blocks:
+  // 13.6 against 14.1 us) and it takes the ring's place.
   const int join = ceil_div(p.tn, p.parts) * p.parts * 512;
-  fs.join = p.tn <= 64 ? join : 0;
+  fs.join = p.tn <= 96 ? join : 0;
   const int fit = std::min(kFewMaxStages, (budget - fs.join) / stage_bytes);
   fs.stages = std::max({2, fs.join > 0 ? 0 : ceil_div(join, stage_bytes),
                         std::min(fit, ceil_div(args.kbt, p.parts))});
