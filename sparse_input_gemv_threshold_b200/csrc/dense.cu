@@ -538,12 +538,14 @@ __device__ __forceinline__ void join_send(uint32_t buf, uint32_t acc, int warp, 
 // tokens (the tile's from `first`), 4 columns a lane, so that a warp reads a
 // token's 512 bytes and writes its 256 in one piece each, and keeps the bias in
 // registers.  kJoin tokens are under way in a warp, without a branch between
-// them; what the first of them read from memory is asked for in the
-// constructor, before the sums are there.
-constexpr int kJoin = 4;
-
+// them: 4 of a linear product (256 x 1024 -> 1024 with K whole 10.2 us, 11.0 with
+// 2), fewer where a token's arithmetic is long, since code that runs once a launch
+// costs what fetching it takes (a backward pass of 1024 / 2816 at one token 19.5 us
+// with 4, 19.0 with 2).  What the first of them read from memory is asked for in
+// the constructor, before the sums are there.
 template <int EPI, bool BF>
 struct Join {
+  static constexpr int kJoin = EPI == DENSE_LINEAR ? 4 : EPI == DENSE_GRAD ? 2 : 1;
   static constexpr int kLanes = EPI == DENSE_GATED ? 16 : 32;   // lanes of a token
   static constexpr int kStep = 256 / kLanes;                    // tokens that the CTA takes at once
   const DenseArgs& args;
@@ -1252,45 +1254,58 @@ constexpr int kClusters2[kFewCluster + 1] = {0, 296, 148, 93, 71, 56, 45, 37, 33
 
 // Which kernel, and how a few-token launch is split.
 //
-// Up to 64 tokens the launch is bound by reading the weight and two CTAs fit an
-// SM.  K is split until there are 128 CTAs, and on while each keeps 16 stages and
-// the clusters run at once.  Measured on B200 with 16 tokens: 4096 -> 4096 9.1 us
-// with 4 parts against 10.0 with 8 and 9.6 with 3; 11008 -> 4096 17.9 with 8
-// against 18.8 with 4; 4096 -> 11008 17.7 with 3 against 20.3 with 1.
+// Up to 16 tokens the launch is bound by reading the weight and two CTAs share an
+// SM.  K is split until there are 128 CTAs, and on while each keeps 32 stages and
+// the clusters run at once.  Measured on B200 with 16 tokens: 4096 -> 4096 8.6 us
+// with 4 parts against 9.3 with 3; 11008 -> 4096 17.2 with 5 against 17.6 with 8;
+// 4096 -> 11008 17.2 with 2 or 3 against 18.5 with 1.
 //
-// From 65 to 1024 tokens both kernels are in play, bound by what a stage takes to
-// arrive (about 136 KB/us an SM): the few-token kernel with blocks of 64 tokens or
-// more and K split over the SMs, or the pair kernel with its whole and half tiles.
-// The estimates below, in us, pick the faster.  Their constants were fitted to 266
-// shapes of 65 - 1024 tokens, K of 256 - 11008 and 512 - 16384 outputs, each timed
-// with every split that fits: the choice costs 1.0 % over the fastest on average.
-// At 256 tokens: 4096 -> 4096 few 12.7 against pair 20.9 us, 4096 -> 11008 pair 26.2
-// against few 29.5, 1024 -> 1024 few 5.6 against pair 7.7.  Beyond 1024 tokens the
-// pair kernel fills the GPU.
+// Up to 1024 tokens both kernels are in play: the few-token kernel with blocks of
+// 64 tokens or more (or two halves) and K split over the SMs, or the pair kernel
+// with its whole and half tiles.  The estimates below, in us, pick the faster.  A
+// stage takes what its bytes take to arrive at an SM (about 136 KB/us, shared by
+// the CTAs on it) or what the weight of all CTAs takes to arrive from memory; two
+// CTAs share an SM only with blocks of 64 tokens, whose rings are deep enough, and
+// several blocks run only within two waves, so that the second one finds the weight
+// in the L2 cache (400 x 8192 -> 2 x 28672: 576 us in seven, 538 with the pair
+// kernel).  The constants were fitted to 284 shapes of 17 - 1024 tokens, K of 256 - 11008 and
+// 512 - 32768 outputs, each timed with every split that fits: the choice costs
+// 1.2 % over the fastest on average.  At 256 tokens: 4096 -> 4096 few 12.7 against
+// pair 20.9 us, 4096 -> 11008 pair 26.2 against few 29.5, 1024 -> 1024 few 5.6
+// against pair 7.7; at 64, 4096 -> 4096 9.8 us with one CTA an SM against 11.2 with
+// two.  Beyond 1024 tokens the pair kernel fills the GPU.
 DensePlan plan_dense(const DenseGemm& d, int kbt) {
   const DensePlan pair = {true, 0, 0, 0};
   if (d.a_mn || d.rows > 1024) return pair;
   const int shrink = d.epi == DENSE_GATED ? 2 : 1;   // accumulator columns of an output column
   const int cols = d.mats * ceil_div(d.cols * shrink, 128);
-  if (d.rows <= 64) {
-    int parts = std::min({kFewCluster, kbt, std::max({1, kbt / 16, 128 / cols})});
+  if (d.rows <= 16) {
+    int parts = std::min({kFewCluster, kbt, std::max({1, kbt / 32, 128 / cols})});
     while (parts > 1 && cols > kClusters2[parts]) --parts;
-    return {false, ceil_div(d.rows, 16) * 16, parts, 2};
+    return {false, 16, parts, 2};
   }
   const int tiles = ceil_div(d.rows, 256) * d.mats * ceil_div(d.cols * shrink, 256);
   const int waves = tiles / (kNumSMs / 2), left = tiles % (kNumSMs / 2);
-  double best = 3.9 + kbt * (0.32 * waves + (left == 0 ? 0.0 : left <= kNumSMs / 4 ? 0.245 : 0.335));
+  double best = 4.1 + kbt * (0.36 * waves + (left == 0 ? 0.0 : left <= kNumSMs / 4 ? 0.25 : 0.33));
   DensePlan plan = pair;
-  for (int blocks = ceil_div(d.rows, 256); blocks <= ceil_div(d.rows, 64); ++blocks) {
+  for (int blocks = ceil_div(d.rows, 256); blocks <= std::max(2, ceil_div(d.rows, 64)); ++blocks) {
     const int tn = ceil_div(ceil_div(d.rows, blocks), 16) * 16, few = blocks * cols;
-    for (int parts = 1; parts <= std::min(kFewCluster, kbt); ++parts) {
-      const double stage = (16.0 + tn / 8.0) / 136.0, join = tn * (0.01 + 0.02 * (parts - 1) / parts);
-      const double t = ceil_div(few, kClusters1[parts]) * (2.6 + ceil_div(kbt, parts) * stage + join);
-      if (t < best) {
-        best = t;
-        plan = {false, tn, parts, 1};
+    for (int per_sm = 1; per_sm <= (tn <= 64 ? 2 : 1); ++per_sm)
+      for (int parts = 1; parts <= std::min(kFewCluster, kbt); ++parts) {
+        auto wave = [&](int clusters) {
+          const int ctas = clusters * parts, sms = std::min(ctas, kNumSMs * per_sm);
+          const double fill = (16.0 + tn / 8.0) / (ctas <= kNumSMs ? 136.0 : 68.0), read = 16.0 * sms / 7600.0;
+          return 2.0 + 0.3 * (per_sm - 1) + ceil_div(kbt, parts) * std::max(fill, read) +
+                 tn * (0.01 + 0.02 * (parts - 1) / parts);
+        };
+        const int fit = per_sm == 2 ? kClusters2[parts] : kClusters1[parts], full = (few - 1) / fit;
+        if (full > 1 && blocks > 1) break;   // each block reads the weight again
+        const double t = full * wave(fit) + wave(few - full * fit);
+        if (t < best) {
+          best = t;
+          plan = {false, tn, parts, per_sm};
+        }
       }
-    }
   }
   return plan;
 }
