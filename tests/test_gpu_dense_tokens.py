@@ -626,7 +626,7 @@ def test_outputs_beyond_32_bit_offsets(sig):
 
 
 # the listed kernels' borders: one block of tokens and several in the few-token
-# kernel, its join in its own place (to 64 tokens) and in the ring's, odd numbers
+# kernel, its join in its own place (to 96 tokens) and in the ring's, odd numbers
 # of parts along K, whole and half tiles of the pair kernel, one and many waves
 @pytest.mark.parametrize("rows,K,N", [
     (15, 64, 4096), (17, 640, 128), (48, 1024, 384), (63, 4096, 1000), (65, 1024, 136), (66, 11008, 136),
@@ -636,6 +636,30 @@ def test_linear_kernel_borders(sig, rows, K, N):
     for dtype in TYPES:
         check_linear(sig, rows, K, N, dtype, "gelu", True, True, seed=rows)
         check_linear(sig, rows, K, N, dtype, "none", False, False, seed=rows + 7)
+
+
+# blocks of 16 to 256 tokens joined from 1 to 8 parts: shares of a part that end
+# within a group of 16 tokens, a last block of a few tokens (fewer than there are
+# parts), one and two CTAs an SM, the join beside the ring and in its place
+@pytest.mark.parametrize("rows,K,N", [
+    (5, 520, 8), (16, 11008, 4096), (17, 136, 264), (31, 520, 1000), (33, 520, 136), (49, 11008, 520),
+    (81, 11008, 1000), (127, 4096, 2816), (129, 520, 520), (129, 4096, 2816), (177, 11008, 1000),
+    (193, 11008, 264), (209, 11008, 1000), (241, 11008, 2816), (255, 64, 8200), (257, 11008, 520),
+    (257, 4096, 2816), (333, 4096, 520), (333, 4096, 2816), (400, 4096, 520), (500, 11008, 1000),
+    (641, 4096, 136), (641, 11008, 264), (777, 520, 136), (777, 11008, 520)])
+def test_join_of_the_parts(sig, rows, K, N):
+    for dtype in TYPES:
+        check_linear(sig, rows, K, N, dtype, "silu", True, True, seed=rows + 3)
+        check_linear(sig, rows, K, N, dtype, "none", False, False, seed=rows + 4)
+
+
+@pytest.mark.parametrize("rows,m,f,act", [
+    (17, 520, 264, "gelu"), (33, 2048, 1000, "silu"), (65, 264, 2056, "gelu_tanh"), (95, 4096, 392, "relu"),
+    (130, 1024, 136, "none"), (255, 72, 2104, "silu"), (401, 1024, 520, "silu")])
+def test_joins_of_the_gated_block(sig, rows, m, f, act):
+    for dtype in TYPES:
+        test_gated_mlp(sig, dtype, rows, m, f, act)
+        test_gated_mlp_backward(sig, dtype, rows, m, f, act)
 
 
 @pytest.mark.parametrize("rows", [600, 1500])
