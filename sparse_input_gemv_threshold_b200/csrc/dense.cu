@@ -1265,15 +1265,17 @@ constexpr int kClusters2[kFewCluster + 1] = {0, 296, 148, 93, 71, 56, 45, 37, 33
 // with its whole and half tiles.  The estimates below, in us, pick the faster.  A
 // stage takes what its bytes take to arrive at an SM (about 136 KB/us, shared by
 // the CTAs on it) or what the weight of all CTAs takes to arrive from memory; two
-// CTAs share an SM only with blocks of 64 tokens, whose rings are deep enough, and
-// several blocks run only within two waves, so that the second one finds the weight
-// in the L2 cache (400 x 8192 -> 2 x 28672: 576 us in seven, 538 with the pair
-// kernel).  The constants were fitted to 284 shapes of 17 - 1024 tokens, K of 256 - 11008 and
-// 512 - 32768 outputs, each timed with every split that fits: the choice costs
-// 1.2 % over the fastest on average.  At 256 tokens: 4096 -> 4096 few 12.7 against
-// pair 20.9 us, 4096 -> 11008 pair 26.2 against few 29.5, 1024 -> 1024 few 5.6
-// against pair 7.7; at 64, 4096 -> 4096 9.8 us with one CTA an SM against 11.2 with
-// two.  Beyond 1024 tokens the pair kernel fills the GPU.
+// CTAs share an SM with blocks of at most 128 tokens and K whole (128 x 4096 ->
+// 11008 in three parts 21.8 us, 20.0 alone with K whole), and several blocks run only
+// within two waves, so that the second one finds the weight in the L2 cache (400 x
+// 8192 -> 2 x 28672: 576 us in seven, 538 with the pair kernel).  The constants were
+// fitted to 321 shapes of 17 - 1024 tokens, K of 256 - 11008 and 512 - 32768
+// outputs, each timed with every split that fits: the choice costs 1.1 % over the
+// fastest on average.  At 256 tokens: 4096 -> 4096 few 12.7 against pair 20.9 us,
+// 4096 -> 11008 pair 26.2 against few 29.5, 1024 -> 1024 few 5.6 against pair 7.7.
+// At 64: 4096 -> 4096 9.8 us with one CTA an SM against 11.2 with two, 2048 -> 20480
+// 17.6 with two against 23.7 with one.  Beyond 1024 tokens the pair kernel fills the
+// GPU.
 DensePlan plan_dense(const DenseGemm& d, int kbt) {
   const DensePlan pair = {true, 0, 0, 0};
   if (d.a_mn || d.rows > 1024) return pair;
@@ -1290,8 +1292,8 @@ DensePlan plan_dense(const DenseGemm& d, int kbt) {
   DensePlan plan = pair;
   for (int blocks = ceil_div(d.rows, 256); blocks <= std::max(2, ceil_div(d.rows, 64)); ++blocks) {
     const int tn = ceil_div(ceil_div(d.rows, blocks), 16) * 16, few = blocks * cols;
-    for (int per_sm = 1; per_sm <= (tn <= 64 ? 2 : 1); ++per_sm)
-      for (int parts = 1; parts <= std::min(kFewCluster, kbt); ++parts) {
+    for (int per_sm = 1; per_sm <= (tn <= 128 ? 2 : 1); ++per_sm)
+      for (int parts = 1; parts <= (per_sm == 2 ? 1 : std::min(kFewCluster, kbt)); ++parts) {
         auto wave = [&](int clusters) {
           const int ctas = clusters * parts, sms = std::min(ctas, kNumSMs * per_sm);
           const double fill = (16.0 + tn / 8.0) / (ctas <= kNumSMs ? 136.0 : 68.0), read = 16.0 * sms / 7600.0;
@@ -1368,12 +1370,13 @@ cudaError_t launch_few(const DensePlan& p, const DenseMaps& maps, const DenseArg
   // shared memory of a CTA: half of the SM's 228 KB (less 1 KB a CTA), or what one CTA may have
   const int budget = (p.per_sm == 2 ? kSmemPerSm / 2 - 1024 : kSmemPerCta) - extra;
   // The join: tn tokens x 128 columns of float32, rounded up to whole ranks.
-  // Up to 96 tokens it has a place of its own, which saves the cluster barrier
+  // Up to 96 tokens (32 where two CTAs share an SM) it has a place of its own, which saves the cluster barrier
   // that says that every ring is free (96 x 4096 -> 4096: 10.6 against 11.1 us);
   // above, the ring would lose too many stages (256 x 4096 -> 4096 in two blocks:
-  // 13.6 against 14.1 us) and it takes the ring's place.
+  // 13.6 against 14.1 us; 80 x 4096 -> 22016 with two CTAs an SM: 32 against 44) and
+  // it takes the ring's place.
   const int join = ceil_div(p.tn, p.parts) * p.parts * 512;
-  fs.join = p.tn <= 96 ? join : 0;
+  fs.join = p.tn <= (p.per_sm == 2 ? 32 : 96) ? join : 0;
   const int fit = std::min(kFewMaxStages, (budget - fs.join) / stage_bytes);
   fs.stages = std::max({2, fs.join > 0 ? 0 : ceil_div(join, stage_bytes),
                         std::min(fit, ceil_div(args.kbt, p.parts))});
