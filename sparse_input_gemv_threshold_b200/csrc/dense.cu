@@ -1365,6 +1365,9 @@ cudaError_t launch_few(const DensePlan& p, const DenseMaps& maps, const DenseArg
   FewShape fs;
   fs.tn = p.tn;
   fs.tmem = 32;
+  // CTAs that wait for columns hold up their cluster, so those that an SM's shared
+  // memory lets in, of one launch or several, need no more than its 512: 128 columns
+  // come with at least 54 KB, 256 with 104 KB.
   while (fs.tmem < p.tn) fs.tmem *= 2;
   const int stage_bytes = (int)kOperand + p.tn * 128, extra = 1024 + (int)sizeof(FewBars);
   // shared memory of a CTA: half of the SM's 228 KB (less 1 KB a CTA), or what one CTA may have
