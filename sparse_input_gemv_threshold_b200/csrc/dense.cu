@@ -52,6 +52,7 @@ struct DenseArgs {
   int tm, tn;          // tiles down, and across one weight
   int rows2, cols2, tm2, tn2;   // pair kernel: the second product of the launch (weight 2), if any
   int whole, items;    // pair kernel: tiles taken whole, and all items of the walk
+  int group;           // tall kernel: token tiles walked together
   int mats;
   int outs;            // outputs to store (DENSE_GATED: 1, or 3 with g and u)
   int act;
@@ -1066,6 +1067,267 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
 }
 
 // ---------------------------------------------------------------------------
+// Persistent CTA pairs with the tokens as N: tiles of 256 accumulator columns x
+// any multiple of 16 tokens up to 256
+//
+// The same walk, two accumulators and warps' roles, but the weight is the MMA's M
+// operand (128 of its columns a CTA) and the tokens, of which each CTA brings
+// half, are N: 777 tokens cost 832 in four tiles, not 1024, and the height of the
+// tiles can be chosen so that they fill whole waves.  A thread holds one output
+// column of 16 tokens at a time; four warps turn them over in shared memory, from
+// which each takes four tokens, 4 columns a lane.
+// ---------------------------------------------------------------------------
+constexpr uint32_t kTurn = 16 * 128 * 4;   // 16 tokens x 128 columns of float32; four warps have two
+constexpr int kTallMaxStages = 8;
+
+struct TallBars {
+  unsigned long long full[kTallMaxStages];         // used in the leader
+  unsigned long long empty[kTallMaxStages];
+  unsigned long long acc_full[2], acc_empty[2];    // acc_empty used in the leader
+  unsigned long long done;
+  uint32_t tmem_base;
+  int abort_flag;
+  int consumed;
+};
+
+// Item t of the walk: token tile m, column tile n.  The token tiles of a group run
+// side by side through all columns, so that a wave's pairs share their weight and
+// the group's tokens stay in the L2 cache.
+struct TallPos {
+  int m, n;
+};
+
+__device__ __forceinline__ TallPos tall_at(int t, const DenseArgs& a) {
+  const int per = a.group * a.tn, g0 = t / per * a.group, r = t % per;
+  const int gs = min(a.group, a.tm - g0);
+  return {g0 + r % gs, r / gs};
+}
+
+// Barrier `id` of 128 threads, which all learn whether every one said yes.
+__device__ __forceinline__ bool all_of_128(int id, bool yes) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.and.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(yes ? 1u : 0u), "r"(id)
+      : "memory");
+  return r != 0;
+}
+
+template <bool B_K, int EPI, bool BF>
+__global__ void __launch_bounds__(kPairThreads, 1)
+dense_tall_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__ DenseArgs args, const int tn,
+                  const int S) {
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  const uint32_t x_bytes = (uint32_t)tn * 64u, stage_bytes = kOperand + x_bytes;   // 1024-multiples
+  uint8_t* turns = ring + (size_t)S * stage_bytes;
+  TallBars& sm = *reinterpret_cast<TallBars*>(turns + 4 * kTurn);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  volatile int* abort_flag = &sm.abort_flag;
+  constexpr int kOutCols = EPI == DENSE_GATED ? 64 : 128;   // output columns of a CTA
+
+  if (warp == 9 && lane < 4) prefetch_map(lane < 2 ? &maps.a[lane] : &maps.b[lane - 2]);
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(smem_u32(&sm.full[s]), 1);
+      mbar_init(smem_u32(&sm.empty[s]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&sm.acc_full[s]), 1);
+      mbar_init(smem_u32(&sm.acc_empty[s]), 16);   // the epilogue warps of both CTAs
+    }
+    mbar_init(smem_u32(&sm.done), 1);
+    sm.abort_flag = 0;
+    sm.consumed = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 8) {   // all of tensor memory, as in dense_pair_kernel
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(&sm.tmem_base)),
+                 "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  __syncwarp();
+  cluster_sync();   // both CTAs' barriers exist before anything targets them
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = sm.tmem_base;
+  pdl_wait();
+  pdl_trigger();
+  const long long limit = wait_limit();
+
+  int issued = 0;   // stages whose copies this CTA's producer has issued
+  if (warp == 8) {   // ---- TMA producer (both CTAs): the warp loops, one lane issues ----
+    int s = 0;
+    uint32_t ph = 1;
+    bool go = true;
+    const uint32_t full0 = map_to_rank(smem_u32(&sm.full[0]), 0);
+    for (int t = pair; t < args.items && go; t += pairs) {
+      const TallPos p = tall_at(t, args);
+      const int t0 = p.m * tn + (int)rank * (tn / 2), n0 = (p.n * 2 + (int)rank) * kOutCols;
+      for (int kb = 0; kb < args.kbt; ++kb) {
+        go = __all_sync(kFull, wait_bounded(smem_u32(&sm.empty[s]), ph, abort_flag, limit));
+        if (!go) break;
+        const int seg = kb >= args.kb0 ? 1 : 0;
+        const uint32_t fb = full0 + (uint32_t)s * 8u, w0 = smem_u32(ring) + (uint32_t)s * stage_bytes;
+        if (elect_one()) {
+          if (leader) mbar_expect_tx(smem_u32(&sm.full[s]), 2 * stage_bytes);
+          weight_boxes<B_K, EPI>(maps, args, 0, n0, kb, [&](const CUtensorMap* map, int c0, int c1, uint32_t at) {
+            tma_load_2d_pair(w0 + at, map, c0, c1, fb);
+          });
+          tma_load_2d_pair(w0 + kOperand, &maps.a[seg], (kb - (seg ? args.kb0 : 0)) * kSlab, t0, fb);
+        }
+        __syncwarp();
+        ++issued;
+        if (++s == S) { s = 0; ph ^= 1u; }
+      }
+    }
+  } else if (warp == 9) {   // ---- MMA issuer (the leader's): the warp loops, one lane issues ----
+    if (leader) {
+      const uint32_t idesc = dense_idesc(256, tn, BF, !B_K, true);
+      const uint32_t w_low = slab_low<!B_K>(smem_u32(ring)), x_low = slab_low<false>(smem_u32(ring) + kOperand);
+      int s = 0, count = 0, used = 0;
+      uint32_t ph = 0, at = 0;   // at: the stage's offset in 16-byte units
+      bool go = true;
+      for (int t = pair; t < args.items && go; t += pairs, ++count) {
+        const int slot = count & 1;
+        go = __all_sync(kFull, wait_bounded(smem_u32(&sm.acc_empty[slot]),
+                                            ((uint32_t)(count >> 1) & 1u) ^ 1u, abort_flag, limit));
+        if (!go) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t d = tmem + (uint32_t)slot * 256u;
+        for (int kb = 0; kb < args.kbt; ++kb) {
+          go = __all_sync(kFull, wait_bounded(smem_u32(&sm.full[s]), ph, abort_flag, limit));
+          if (!go) break;
+          asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+          ++used;
+          if (elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kSlab / 16; ++k)
+              mma_f16<2>(d, slab_desc(w_low + at + k * slab_step<!B_K>),
+                         slab_desc(x_low + at + k * slab_step<false>), idesc, (kb > 0 || k > 0) ? 1u : 0u);
+            commit_pair(smem_u32(&sm.empty[s]));
+            if (kb == args.kbt - 1) commit_pair(smem_u32(&sm.acc_full[slot]));
+          }
+          __syncwarp();
+          at += stage_bytes >> 4;
+          if (++s == S) { s = 0; at = 0; ph ^= 1u; }
+        }
+      }
+      if (lane == 0) sm.consumed = used;
+      if (elect_one()) commit_pair(smem_u32(&sm.done));   // completes once every issued MMA has finished
+      __syncwarp();
+    }
+  } else {   // ---- epilogue: two times four warps, groups of 16 tokens in turn ----
+    constexpr int kLanes = kOutCols / 4, kSub = 32 / kLanes;   // lanes of a token, tokens of a warp's access
+    constexpr int kTake = 4 / kSub;                            // accesses for a warp's four tokens
+    const int q = warp & 3, half = warp >> 2;
+    const uint32_t turn = smem_u32(turns) + (uint32_t)half * 2u * kTurn;
+    const uint32_t empty0 = map_to_rank(smem_u32(&sm.acc_empty[0]), 0);
+    const uint32_t empty1 = map_to_rank(smem_u32(&sm.acc_empty[1]), 0);
+    const int mine = q * 4 + lane / kLanes, ch = lane % kLanes * 4;   // this lane's first token of 16, its columns
+    uint32_t set = 0;   // the half of `turn` used next
+    int count = 0;
+    for (int t = pair; t < args.items; t += pairs, ++count) {
+      const TallPos p = tall_at(t, args);
+      const int t0 = p.m * tn, col = (p.n * 2 + (int)rank) * kOutCols + ch;
+      const int groups = (min(tn, args.rows - t0) + 15) / 16;
+      const int slot = count & 1;
+      // what tokens [t0 + 16 g, ..) read besides the sums
+      auto fetch = [&](Extra (&e)[kTake], int g) {
+#pragma unroll
+        for (int i = 0; i < kTake; ++i) {
+          const int row = t0 + g * 16 + mine + i * kSub;
+          e[i] = {make_uint2(0, 0), make_uint2(0, 0)};
+          if (g < groups && row < args.rows && col < args.cols) e[i] = load_extra<EPI>(args, row, col);
+        }
+      };
+      float4 bias = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (EPI == DENSE_LINEAR && args.bias != nullptr && col < args.cols)
+        bias = unpack4<BF>(__ldg(reinterpret_cast<const uint2*>(args.bias + col)));
+      Extra e[kTake];
+      fetch(e, half);
+      // one verdict for the four warps, whose barriers and tensor-memory loads need all of them
+      if (!all_of_128(1 + half, wait_bounded(smem_u32(&sm.acc_full[slot]), (uint32_t)(count >> 1) & 1u,
+                                             abort_flag, limit)))
+        break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      const uint32_t acc = tmem + (uint32_t)slot * 256u + ((uint32_t)(q * 32) << 16);
+      auto release = [&] {   // this warp has read its part of the accumulator
+        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) arrive_remote(slot ? empty1 : empty0);
+      };
+      if (half >= groups) release();
+      with_act(args.act, [&](auto A) {
+#pragma unroll 1
+        for (int g = half; g < groups; g += 2, set ^= 1u) {
+          uint32_t r[16];
+          tmem_start16(r, acc + (uint32_t)(g * 16));
+          Extra next[kTake];
+          fetch(next, g + 2);
+          tmem_wait16(r);
+          if (g + 2 >= groups) release();
+          const uint32_t buf = turn + set * kTurn, to = buf + (uint32_t)(q * 32 + lane) * 4u;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sts_b32(to + i * 512u, r[i]);
+          // the other set is free again once every warp is here
+          asm volatile("barrier.cta.sync.aligned %0, 128;" ::"r"(1 + half) : "memory");
+          uint2 o[3][kTake];
+#pragma unroll
+          for (int i = 0; i < kTake; ++i) {
+            const uint32_t f = buf + (uint32_t)((mine + i * kSub) * 128 + ch) * 4u;
+            const float4 v = lds_f32x4(f);
+            float4 w = {};
+            if constexpr (EPI == DENSE_GATED) w = lds_f32x4(f + 256u);
+            finish4<EPI, BF, decltype(A)::value>(v, w, bias, e[i], o[0][i], o[1][i], o[2][i]);
+          }
+#pragma unroll
+          for (int i = 0; i < kTake; ++i) {
+            const int row = t0 + g * 16 + mine + i * kSub;
+            if (row < args.rows && col < args.cols) {
+              const int64_t at = (int64_t)row * args.ldo + col;
+              *reinterpret_cast<uint2*>(args.o[0] + at) = o[0][i];
+              if (EPI == DENSE_GRAD || (EPI == DENSE_GATED && args.outs == 3)) {
+                *reinterpret_cast<uint2*>(args.o[1] + at) = o[1][i];
+                *reinterpret_cast<uint2*>(args.o[2] + at) = o[2][i];
+              }
+            }
+            e[i] = next[i];
+          }
+        }
+      });
+    }
+  }
+
+  __syncthreads();
+  wait_drain(smem_u32(&sm.done), 0u);
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (warp == 8 && lane == 0 && *abort_flag) {
+    // after a give-up: the copies that were issued land before shared memory goes
+    if (leader)
+      for (int it = sm.consumed; it < issued; ++it)
+        wait_drain(smem_u32(&sm.full[it % S]), (uint32_t)(it / S) & 1u);
+    const long long start = clock64();
+    while (clock64() - start < 40000) {
+    }
+  }
+  __syncthreads();
+  cluster_sync();
+  if (warp == 8)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // Few tokens: 128 output columns x up to 256 tokens a tile, K split over a cluster
 //
 // A stage carries 16 KB of weight and only 128 bytes a token, and a block of
@@ -1237,10 +1499,13 @@ bool map16(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a product is run: by the pair kernel, or by the few-token kernel with
-// tiles of tn tokens, `parts` CTAs along K and per_sm CTAs resident on an SM.
+// How a product is run: by the pair kernel, by the tall kernel with tiles of tn
+// tokens, or by the few-token kernel with tiles of tn tokens, `parts` CTAs along K
+// and per_sm CTAs resident on an SM.
+enum DenseKind { DENSE_PAIR, DENSE_TALL, DENSE_FEW };
+
 struct DensePlan {
-  bool pair;
+  DenseKind kind;
   int tn, parts, per_sm;
 };
 
@@ -1260,37 +1525,55 @@ constexpr int kClusters2[kFewCluster + 1] = {0, 296, 148, 93, 71, 56, 45, 37, 33
 // with 4 parts against 9.3 with 3; 11008 -> 4096 17.2 with 5 against 17.6 with 8;
 // 4096 -> 11008 17.2 with 2 or 3 against 18.5 with 1.
 //
-// Up to 1024 tokens both kernels are in play: the few-token kernel with blocks of
-// 64 tokens or more (or two halves) and K split over the SMs, or the pair kernel
-// with its whole and half tiles.  The estimates below, in us, pick the faster.  A
-// stage takes what its bytes take to arrive at an SM (about 136 KB/us, shared by
-// the CTAs on it) or what the weight of all CTAs takes to arrive from memory; two
-// CTAs share an SM with blocks of at most 128 tokens and K whole (128 x 4096 ->
-// 11008 in three parts 21.8 us, 20.0 alone with K whole), and several blocks run only
-// within two waves, so that the second one finds the weight in the L2 cache (400 x
-// 8192 -> 2 x 28672: 576 us in seven, 538 with the pair kernel).  The constants were
-// fitted to 321 shapes of 17 - 1024 tokens, K of 256 - 11008 and 512 - 32768
-// outputs, each timed with every split that fits: the choice costs 1.1 % over the
-// fastest on average.  At 256 tokens: 4096 -> 4096 few 12.7 against pair 20.9 us,
-// 4096 -> 11008 pair 26.2 against few 29.5, 1024 -> 1024 few 5.6 against pair 7.7.
-// At 64: 4096 -> 4096 9.8 us with one CTA an SM against 11.2 with two, 2048 -> 20480
-// 17.6 with two against 23.7 with one.  Beyond 1024 tokens the pair kernel fills the
-// GPU.
+// Above, the estimates below, in us, pick the fastest of what is in play.
+//
+// The few-token kernel, to 1024 tokens, with blocks of 64 tokens or more (or two
+// halves) and K split over the SMs.  A stage takes what its bytes take to arrive at
+// an SM (about 136 KB/us, shared by the CTAs on it) or what the weight of all CTAs
+// takes to arrive from memory; two CTAs share an SM with blocks of at most 128
+// tokens and K whole (128 x 4096 -> 11008 in three parts 21.8 us, 20.0 alone with K
+// whole), and several blocks run only within two waves, so that the second one finds
+// the weight in the L2 cache (400 x 8192 -> 2 x 28672: 576 us in seven, 538 with the
+// pair kernel).  Fitted to 321 shapes of 17 - 1024 tokens, K of 256 - 11008 and 512 -
+// 32768 outputs, each timed with every split that fits: the choice costs 1.1 % over
+// the fastest on average.  At 64 tokens: 4096 -> 4096 9.8 us with one CTA an SM
+// against 11.2 with two, 2048 -> 20480 17.6 with two against 23.7 with one.
+//
+// The tall kernel, with the tile height whose waves cost least, and the pair kernel
+// with its whole and half tiles.  Fitted to 154 shapes of 128 - 4096 tokens, K of 512
+// - 22016 and 1024 - 22016 outputs, the choice costs 0.6 % over the fastest.  At 256
+// tokens: 4096 -> 4096 few 13.4 us, tall 17.8, pair 21.2; at 777: 4096 -> 11008 tall
+// 56.1, pair 67.7; 4096 x 4096 -> 22016 tall 537, pair 568; 4096 x 1024 -> 1024 pair
+// 11.1, tall 12.1.
+constexpr int kGroupTiles = 16;   // token tiles the tall kernel walks together (4096 x 4096 -> 11008 in
+                                  // tiles of 208: 276 us, 281 with 4; 16384 x 4096 -> 4096: 405, 413 with all)
 DensePlan plan_dense(const DenseGemm& d, int kbt) {
-  const DensePlan pair = {true, 0, 0, 0};
-  if (d.a_mn || d.rows > 1024) return pair;
+  const DensePlan pair = {DENSE_PAIR, 0, 0, 0};
+  if (d.a_mn) return pair;
   const int shrink = d.epi == DENSE_GATED ? 2 : 1;   // accumulator columns of an output column
   const int cols = d.mats * ceil_div(d.cols * shrink, 128);
   if (d.rows <= 16) {
     int parts = std::min({kFewCluster, kbt, std::max({1, kbt / 32, 128 / cols})});
     while (parts > 1 && cols > kClusters2[parts]) --parts;
-    return {false, 16, parts, 2};
+    return {DENSE_FEW, 16, parts, 2};
   }
   const int tiles = ceil_div(d.rows, 256) * d.mats * ceil_div(d.cols * shrink, 256);
   const int waves = tiles / (kNumSMs / 2), left = tiles % (kNumSMs / 2);
   double best = 4.1 + kbt * (0.36 * waves + (left == 0 ? 0.0 : left <= kNumSMs / 4 ? 0.25 : 0.33));
   DensePlan plan = pair;
-  for (int blocks = ceil_div(d.rows, 256); blocks <= std::max(2, ceil_div(d.rows, 64)); ++blocks) {
+  const int least = ceil_div(d.rows, 256);
+  for (int blocks = least; blocks <= std::min(least + 16, ceil_div(d.rows, 64)); ++blocks) {
+    const int tn = ceil_div(ceil_div(d.rows, blocks), 16) * 16;
+    const double stage = std::max(0.00125 * tn, (16.0 + tn / 16.0) / 115.0);
+    const int64_t items = (int64_t)ceil_div(d.rows, tn) * ceil_div(d.cols * shrink, 256);
+    const double t = 3.6 + 0.005 * tn + ceil_div(items, kNumSMs / 2) * (kbt * stage + 0.5);
+    if (t < best) {
+      best = t;
+      plan = {DENSE_TALL, tn, 1, 1};
+    }
+  }
+  if (d.rows > 1024) return plan;
+  for (int blocks = least; blocks <= std::max(2, ceil_div(d.rows, 64)); ++blocks) {
     const int tn = ceil_div(ceil_div(d.rows, blocks), 16) * 16, few = blocks * cols;
     for (int per_sm = 1; per_sm <= (tn <= 128 ? 2 : 1); ++per_sm)
       for (int parts = 1; parts <= (per_sm == 2 ? 1 : std::min(kFewCluster, kbt)); ++parts) {
@@ -1305,7 +1588,7 @@ DensePlan plan_dense(const DenseGemm& d, int kbt) {
         const double t = full * wave(fit) + wave(few - full * fit);
         if (t < best) {
           best = t;
-          plan = {false, tn, parts, per_sm};
+          plan = {DENSE_FEW, tn, parts, per_sm};
         }
       }
   }
@@ -1389,11 +1672,25 @@ cudaError_t launch_few(const DensePlan& p, const DenseMaps& maps, const DenseArg
       stream, maps, args, fs);
 }
 
+template <bool B_K, int EPI, bool BF>
+cudaError_t launch_tall(const DensePlan& p, const DenseMaps& maps, const DenseArgs& args,
+                        cudaStream_t stream) {
+  const int stage_bytes = (int)kOperand + p.tn * 64, rest = 4 * (int)kTurn + (int)sizeof(TallBars) + 1024;
+  const int stages = std::min(kTallMaxStages, (kSmemPerCta - rest) / stage_bytes);
+  const int pairs = std::min(args.items, kNumSMs / 2);
+  // all of an SM's shared memory, whatever the ring takes: nothing else that uses
+  // tensor memory may run beside a CTA that holds all of it
+  return launch_cluster<&dense_tall_kernel<B_K, EPI, BF>>(dim3(2 * pairs), kPairThreads, 2, kSmemPerCta, stream,
+                                                          maps, args, p.tn, stages);
+}
+
 template <bool A_MN, bool B_K, int EPI, bool BF>
 cudaError_t launch_as(const DensePlan& p, const DenseMaps& maps, const DenseArgs& args,
                       cudaStream_t stream) {
-  if (p.pair) return launch_pair_kernel<A_MN, B_K, EPI, BF>(maps, args, stream);
-  if constexpr (!A_MN) return launch_few<B_K, EPI, BF>(p, maps, args, stream);
+  if (p.kind == DENSE_PAIR) return launch_pair_kernel<A_MN, B_K, EPI, BF>(maps, args, stream);
+  if constexpr (!A_MN)
+    return p.kind == DENSE_TALL ? launch_tall<B_K, EPI, BF>(p, maps, args, stream)
+                                : launch_few<B_K, EPI, BF>(p, maps, args, stream);
   return cudaErrorInvalidValue;
 }
 
@@ -1419,10 +1716,13 @@ cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream) {
   a.cols = (int)d.cols;
   a.kb0 = kb;
   a.kbt = kbt;
-  a.tm = ceil_div(d.rows, p.pair ? 256 : p.tn);
-  a.tn = ceil_div(d.cols, (p.pair ? 256 : 128) / (dual ? 2 : 1));
+  const bool pair = p.kind == DENSE_PAIR;
+  a.tm = ceil_div(d.rows, pair ? 256 : p.tn);
+  a.tn = ceil_div(d.cols, (p.kind == DENSE_FEW ? 128 : 256) / (dual ? 2 : 1));
   a.mats = d.mats;
-  if (p.pair) {
+  a.items = a.tm * a.tn;
+  a.group = kGroupTiles;
+  if (pair) {
     if (d.also != nullptr) {
       a.rows2 = (int)d.also->rows;
       a.cols2 = (int)d.also->cols;
@@ -1447,17 +1747,18 @@ cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream) {
   const int n_a = d.two_segments ? 2 : 1, n_b = (d.two_segments || d.mats == 2 || dual) ? 2 : 1;
   for (int i = 0; i < n_a; ++i)
     if (!(d.a_mn ? map16(&maps.a[i], d.a[i], d.rows, d.K, d.lda, kSlab)
-                 : map16(&maps.a[i], d.a[i], d.K, d.rows, d.lda, p.pair ? kTile : p.tn)))
+                 : map16(&maps.a[i], d.a[i], d.K, d.rows, d.lda,
+                          pair ? kTile : p.kind == DENSE_TALL ? p.tn / 2 : p.tn)))
       return cudaErrorInvalidValue;
   for (int i = 0; i < n_b; ++i)
-    if (!(d.b_k ? map16(&maps.b[i], d.b[i], d.K, d.cols, d.ldb, p.pair ? 64 : kTile)
+    if (!(d.b_k ? map16(&maps.b[i], d.b[i], d.K, d.cols, d.ldb, pair ? 64 : kTile)
                 : map16(&maps.b[i], d.b[i], d.cols, d.K, d.ldb, kSlab)))
       return cudaErrorInvalidValue;
   // the kernels prefetch every map: the unused ones repeat another
   if (n_a < 2) maps.a[1] = maps.a[0];
   if (n_b < 2) maps.b[1] = maps.b[0];
   maps.b[2] = maps.b[0];
-  if (p.pair) {   // the pair kernel reads its other inputs and stores its outputs with TMA
+  if (pair) {   // the pair kernel reads its other inputs and stores its outputs with TMA
     const int width = d.epi == DENSE_GRAD ? 32 : 64;
     const uint16_t* r[2] = {d.epi == DENSE_GRAD ? d.g : d.residual, d.epi == DENSE_GRAD ? d.u : nullptr};
     for (int i = 0; i < 3; ++i)
