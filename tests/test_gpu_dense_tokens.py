@@ -662,6 +662,76 @@ def test_joins_of_the_gated_block(sig, rows, m, f, act):
         test_gated_mlp_backward(sig, dtype, rows, m, f, act)
 
 
+# the pairs with the tokens as N: tiles of 64 to 256 tokens, one wave and many, more
+# token tiles than are walked together, last tiles of a few tokens and columns
+@pytest.mark.parametrize("rows,K,N", [
+    (333, 2048, 5000), (515, 520, 8200), (777, 1000, 8200), (900, 2048, 8200), (1025, 520, 1000),
+    (1281, 1000, 1000), (1300, 1000, 8200), (1500, 2048, 8200), (2100, 1000, 1000), (6000, 2048, 2056)])
+def test_tall_tiles(sig, rows, K, N):
+    for dtype in TYPES:
+        check_linear(sig, rows, K, N, dtype, "gelu", True, True, seed=rows + 5)
+        check_linear(sig, rows, K, N, dtype, "none", False, False, seed=rows + 6)
+
+
+@pytest.mark.parametrize("rows,m,f,act", [
+    (520, 1000, 2120, "silu"), (777, 1024, 2816, "gelu_tanh"), (1025, 520, 520, "relu"), (1281, 1000, 1000, "gelu"),
+    (2101, 1000, 1000, "silu")])
+def test_tall_tiles_of_the_gated_block(sig, rows, m, f, act):
+    for dtype in TYPES:
+        test_gated_mlp(sig, dtype, rows, m, f, act)
+        test_gated_mlp_backward(sig, dtype, rows, m, f, act)
+
+
+def test_tall_tiles_strided_in_place_and_beside_nan(sig):
+    import torch
+    rows, K, N = 1281, 1000, 1000
+    buf = torch.full((rows + 2, K + 40), float("nan"), dtype=torch.float16, device="cuda")
+    X = buf[1:rows + 1, 16:16 + K]
+    X.copy_(normal(150, rows, K))
+    W = normal(151, K, N, scale=K ** -0.5)
+    out = torch.full((rows + 1, N + 56), 7.0, dtype=torch.float16, device="cuda")
+    Y = out[:rows, 24:24 + N]
+    Y.copy_(normal(152, rows, N))
+    y, e = product(X, W)
+    y = y + Y.double()
+    sig.linear_act(X, W, residual=Y, Y=Y)
+    within(Y, y, rounding(y, e + U * y.abs(), "fp16"), "in place, strided")
+    assert bool((out[:, :24] == 7).all()) and bool((out[:, 24 + N:] == 7).all()) and bool((out[rows] == 7).all())
+    # NaN and infinity stay in their rows and columns
+    X = X.contiguous()
+    clean = sig.linear_act(X, W)
+    X[700, 3], W[5, 999] = float("nan"), float("inf")
+    Y = sig.linear_act(X, W)
+    assert bool(Y[700].isnan().all()) and not bool(Y[:, 999].isfinite().any())
+    keep = [r for r in range(rows) if r != 700]
+    assert torch.equal(Y[keep, :999], clean[keep, :999])
+
+
+def test_tall_tiles_give_up_and_recover(sig):
+    """Waits that give up at once, in the producer, the issuer and the epilogues,
+    end the launch with an error, and the calls after it are right."""
+    import torch
+    args = backward_inputs(1281, 1000, 1000, "bf16", seed=160)
+    R = normal(170, 1281, 1000, dtype="bf16")
+
+    def run():
+        return [sig.linear_act(args[1], args[4], residual=R), sig.gated_mlp(args[1], *args[4:]),
+                *sig.gated_mlp_backward(*args)]
+    want = run()
+    assert sig.take_device_error() == 0
+    for limit in (1, 64, 20000):
+        try:
+            sig.set_wait_limit(limit)
+            run()
+            torch.cuda.synchronize()
+            assert limit > 64 or sig.take_device_error() != 0
+        finally:
+            sig.set_wait_limit(0)
+            sig.take_device_error()
+        assert all(torch.equal(a, b) for a, b in zip(want, run()))
+        assert sig.take_device_error() == 0
+
+
 @pytest.mark.parametrize("rows", [600, 1500])
 def test_a_wait_that_gives_up_lets_the_epilogues_reads_land(sig, rows):
     """The same for the epilogues that read while they wait: the residual, and g
