@@ -8,16 +8,22 @@
 //                      next.  Bound by the tensor cores at the power limit:
 //                      4096 x 4096 x 4096 fp16 in 91-94 us on B200 (1.5 PFLOP/s,
 //                      0.9 of the measured burst rate; 77 % of the launch with
-//                      the tensor pipe active at 1.55 GHz).
+//                      the tensor pipe active at 1.55 GHz).  Weight gradients, and
+//                      the shapes that its tiles fit better than the tall kernel's.
+//   dense_tall_kernel  persistent, with the weight as the MMA's M operand and the
+//                      tokens as N: tiles of 256 columns x any multiple of 16
+//                      tokens, the height chosen so that the tiles fill whole
+//                      waves.  1300 x 4096 -> 11008 fp16 86 us (1.36 PFLOP/s; the
+//                      tensor pipe active in 88 % of the SMs' active cycles).
 //   dense_few_kernel   few tokens, bound by reading the weight: the weight is the
 //                      MMA's M operand (128 of its columns, one a tensor-memory
 //                      lane) and the tokens its N operand; one tile per cluster,
 //                      whose CTAs each take a part of K and join their float32
 //                      sums through distributed shared memory in a fixed order:
 //                      no workspace, no atomics, the same bits in every run.
-//                      16 tokens 4096 -> 11008: 17.5 us, 5.2 TB/s of weight
+//                      16 tokens 4096 -> 11008: 17.4 us, 5.2 TB/s of weight
 //                      (0.79 of the measured copy rate); 1 token 4096 -> 4096
-//                      8.5 us, of which 5.1 are the weight at that rate.
+//                      8.4 us, of which 5.1 are the weight at that rate.
 #include "common.cuh"
 #include "dense.h"
 #include "internal.h"
