@@ -1533,17 +1533,18 @@ constexpr int kClusters2[kFewCluster + 1] = {0, 296, 148, 93, 71, 56, 45, 37, 33
 //
 // Above, the estimates below, in us, pick the fastest of what is in play.
 //
-// The few-token kernel, to 1024 tokens, with blocks of 64 tokens or more (or two
-// halves) and K split over the SMs.  A stage takes what its bytes take to arrive at
-// an SM (about 136 KB/us, shared by the CTAs on it) or what the weight of all CTAs
-// takes to arrive from memory; two CTAs share an SM with blocks of at most 128
-// tokens and K whole (128 x 4096 -> 11008 in three parts 21.8 us, 20.0 alone with K
-// whole), and several blocks run only within two waves, so that the second one finds
-// the weight in the L2 cache (400 x 8192 -> 2 x 28672: 576 us in seven, 538 with the
-// pair kernel).  Fitted to 321 shapes of 17 - 1024 tokens, K of 256 - 11008 and 512 -
-// 32768 outputs, each timed with every split that fits: the choice costs 1.1 % over
-// the fastest on average.  At 64 tokens: 4096 -> 4096 9.8 us with one CTA an SM
-// against 11.2 with two, 2048 -> 20480 17.6 with two against 23.7 with one.
+// The few-token kernel, to 4096 tokens (2048 x 4096 -> 512 12.8 us, the others 18.2),
+// with blocks of 64 tokens or more (or two halves) and K split over the SMs.  A stage
+// takes what its bytes take to arrive at an SM (about 136 KB/us, shared by the CTAs
+// on it) or what the weight of all CTAs takes to arrive from memory and the L2 cache;
+// two CTAs share an SM with blocks of at most 128 tokens and K whole (128 x 4096 ->
+// 11008 in three parts 21.8 us, 20.0 alone with K whole), and several blocks run only
+// within two waves, so that the second one finds the weight in the cache (400 x 8192
+// -> 2 x 28672: 576 us in seven, 538 with the pair kernel).  Fitted to 321 shapes of
+// 17 - 1024 tokens, K of 256 - 11008 and 512 - 32768 outputs, each timed with every
+// split that fits: the choice costs 0.9 % over the fastest on average.  At 64 tokens:
+// 4096 -> 4096 9.8 us with one CTA an SM against 11.2 with two, 2048 -> 20480 17.6
+// with two against 23.7 with one.
 //
 // The tall kernel, with the tile height whose waves cost least, and the pair kernel
 // with its whole and half tiles.  Fitted to 154 shapes of 128 - 4096 tokens, K of 512
@@ -1578,19 +1579,20 @@ DensePlan plan_dense(const DenseGemm& d, int kbt) {
       plan = {DENSE_TALL, tn, 1, 1};
     }
   }
-  if (d.rows > 1024) return plan;
+  if (d.rows > 4096) return plan;
   for (int blocks = least; blocks <= std::max(2, ceil_div(d.rows, 64)); ++blocks) {
+    if (blocks > 1 && blocks * cols > 2 * kClusters2[1]) break;   // more than two waves, each block reads the weight again
     const int tn = ceil_div(ceil_div(d.rows, blocks), 16) * 16, few = blocks * cols;
     for (int per_sm = 1; per_sm <= (tn <= 128 ? 2 : 1); ++per_sm)
       for (int parts = 1; parts <= (per_sm == 2 ? 1 : std::min(kFewCluster, kbt)); ++parts) {
         auto wave = [&](int clusters) {
           const int ctas = clusters * parts, sms = std::min(ctas, kNumSMs * per_sm);
-          const double fill = (16.0 + tn / 8.0) / (ctas <= kNumSMs ? 136.0 : 68.0), read = 16.0 * sms / 7600.0;
-          return 2.0 + 0.3 * (per_sm - 1) + ceil_div(kbt, parts) * std::max(fill, read) +
-                 tn * (0.01 + 0.02 * (parts - 1) / parts);
+          const double fill = (16.0 + tn / 8.0) / (ctas <= kNumSMs ? 136.0 : 68.0), read = 16.0 * sms / 10000.0;
+          return 2.2 + 0.3 * (per_sm - 1) + ceil_div(kbt, parts) * std::max(fill, read) +
+                 tn * (0.0095 + 0.02 * (parts - 1) / parts);
         };
         const int fit = per_sm == 2 ? kClusters2[parts] : kClusters1[parts], full = (few - 1) / fit;
-        if (full > 1 && blocks > 1) break;   // each block reads the weight again
+        if (full > 1 && blocks > 1) break;
         const double t = full * wave(fit) + wave(few - full * fit);
         if (t < best) {
           best = t;

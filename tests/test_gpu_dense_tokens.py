@@ -666,7 +666,8 @@ def test_joins_of_the_gated_block(sig, rows, m, f, act):
 # token tiles than are walked together, last tiles of a few tokens and columns
 @pytest.mark.parametrize("rows,K,N", [
     (333, 2048, 5000), (515, 520, 8200), (777, 1000, 8200), (900, 2048, 8200), (1025, 520, 1000),
-    (1281, 1000, 1000), (1300, 1000, 8200), (1500, 2048, 8200), (2100, 1000, 1000), (6000, 2048, 2056)])
+    (1281, 1000, 1000), (1300, 1000, 8200), (1500, 2048, 8200), (2100, 1000, 1000), (6000, 2048, 2056),
+    (1100, 520, 8200), (1300, 1000, 5000), (5000, 520, 1000)])
 def test_tall_tiles(sig, rows, K, N):
     for dtype in TYPES:
         check_linear(sig, rows, K, N, dtype, "gelu", True, True, seed=rows + 5)
@@ -675,16 +676,17 @@ def test_tall_tiles(sig, rows, K, N):
 
 @pytest.mark.parametrize("rows,m,f,act", [
     (520, 1000, 2120, "silu"), (777, 1024, 2816, "gelu_tanh"), (1025, 520, 520, "relu"), (1281, 1000, 1000, "gelu"),
-    (2101, 1000, 1000, "silu")])
+    (2101, 1000, 1000, "silu"), (777, 1000, 8200, "silu"), (1300, 1000, 5000, "gelu"),
+    (1300, 4104, 1000, "gelu_tanh")])
 def test_tall_tiles_of_the_gated_block(sig, rows, m, f, act):
     for dtype in TYPES:
         test_gated_mlp(sig, dtype, rows, m, f, act)
         test_gated_mlp_backward(sig, dtype, rows, m, f, act)
 
 
-def test_tall_tiles_strided_in_place_and_beside_nan(sig):
+@pytest.mark.parametrize("rows,K,N", [(1281, 1000, 1000), (1300, 1000, 5000)])
+def test_tall_tiles_strided_in_place_and_beside_nan(sig, rows, K, N):
     import torch
-    rows, K, N = 1281, 1000, 1000
     buf = torch.full((rows + 2, K + 40), float("nan"), dtype=torch.float16, device="cuda")
     X = buf[1:rows + 1, 16:16 + K]
     X.copy_(normal(150, rows, K))
@@ -700,19 +702,20 @@ def test_tall_tiles_strided_in_place_and_beside_nan(sig):
     # NaN and infinity stay in their rows and columns
     X = X.contiguous()
     clean = sig.linear_act(X, W)
-    X[700, 3], W[5, 999] = float("nan"), float("inf")
+    X[700, 3], W[5, N - 1] = float("nan"), float("inf")
     Y = sig.linear_act(X, W)
-    assert bool(Y[700].isnan().all()) and not bool(Y[:, 999].isfinite().any())
+    assert bool(Y[700].isnan().all()) and not bool(Y[:, N - 1].isfinite().any())
     keep = [r for r in range(rows) if r != 700]
-    assert torch.equal(Y[keep, :999], clean[keep, :999])
+    assert torch.equal(Y[keep, :N - 1], clean[keep, :N - 1])
 
 
-def test_tall_tiles_give_up_and_recover(sig):
+@pytest.mark.parametrize("rows,m,f", [(1281, 1000, 1000), (1300, 1000, 5000), (1300, 4104, 1000)])
+def test_tall_tiles_give_up_and_recover(sig, rows, m, f):
     """Waits that give up at once, in the producer, the issuer and the epilogues,
     end the launch with an error, and the calls after it are right."""
     import torch
-    args = backward_inputs(1281, 1000, 1000, "bf16", seed=160)
-    R = normal(170, 1281, 1000, dtype="bf16")
+    args = backward_inputs(rows, m, f, "bf16", seed=160)
+    R = normal(170, rows, f, dtype="bf16")
 
     def run():
         return [sig.linear_act(args[1], args[4], residual=R), sig.gated_mlp(args[1], *args[4:]),
