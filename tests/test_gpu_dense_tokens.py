@@ -709,6 +709,36 @@ def test_tall_tiles_strided_in_place_and_beside_nan(sig, rows, K, N):
     assert torch.equal(Y[keep, :N - 1], clean[keep, :N - 1])
 
 
+def test_tall_tiles_on_two_streams_and_in_graphs(sig):
+    """Two captured gated blocks replayed at once on two streams, beside eager
+    calls on a third, give the bits of calls made alone."""
+    import torch
+    rows, m, f = 777, 1000, 8200
+    blocks = [backward_inputs(rows, m, f, "fp16", seed=180 + 10 * i) for i in range(3)]
+
+    def run(b):
+        return [sig.gated_mlp(b[1], *b[4:]), *sig.gated_mlp_backward(*b)]
+    want = [run(b) for b in blocks]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    graphs, got = [], []
+    for b, s in zip(blocks[:2], streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            got.append(run(b))
+        graphs.append(g)
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(streams[2]):
+            eager = run(blocks[2])
+    torch.cuda.synchronize()
+    for a, b in zip(want, got + [eager]):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    assert sig.take_device_error() == 0
+
+
 @pytest.mark.parametrize("rows,m,f", [(1281, 1000, 1000), (1300, 1000, 5000), (1300, 4104, 1000)])
 def test_tall_tiles_give_up_and_recover(sig, rows, m, f):
     """Waits that give up at once, in the producer, the issuer and the epilogues,
