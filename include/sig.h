@@ -606,8 +606,9 @@ SIG_API int gated_mlp(const uint16_t* X, int64_t rows, int64_t ldx, const uint16
  *   dY, X, dX [rows x d_model] with strides.  g, u [rows x d_ff], contiguous.
  *   WgT, WuT, dWgT, dWuT [d_model x d_ff].  WdT, dWdT [d_ff x d_model].
  *   dX nullable; dWgT and dWuT both or neither; dWdT nullable; at least one of
- *   the three.  The gradients are written, not added to.  With rows == 0 the
- *   weight gradients are set to zero.
+ *   the three, but for rows == 0, where dX has no entries (an empty buffer may
+ *   have no address).  The gradients are written, not added to.  With rows == 0
+ *   the weight gradients are set to zero.
  *   ws   sig_workspace_bytes(SIG_OP_GATED_BACKWARD, d_model, d_ff, rows) bytes,
  *        256-byte aligned, for dg, du and h; needs no initialisation and holds
  *        nothing from call to call (NULL for rows == 0).

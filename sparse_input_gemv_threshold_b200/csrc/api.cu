@@ -550,9 +550,7 @@ int gated_mlp_backward(const uint16_t* dY, int64_t lddy, const uint16_t* X, int6
   if (!dense_args(dtype, act)) return SIG_ERR_ARG;
   if (rows < 0 || rows > kMaxRows || !dense_width(d_model) || !dense_width(d_ff))
     return SIG_ERR_SHAPE;
-  if ((dWgT == nullptr) != (dWuT == nullptr) ||
-      (dX == nullptr && dWgT == nullptr && dWdT == nullptr))
-    return SIG_ERR_NULL;
+  if ((dWgT == nullptr) != (dWuT == nullptr)) return SIG_ERR_NULL;
   if (!aligned16(dWgT) || !aligned16(dWuT) || !aligned16(dWdT)) return SIG_ERR_ALIGN;
   cudaStream_t st = (cudaStream_t)stream;
   if (rows == 0) {   // no tokens: the weight gradients are zero
@@ -563,7 +561,7 @@ int gated_mlp_backward(const uint16_t* dY, int64_t lddy, const uint16_t* X, int6
     return SIG_OK;
   }
   if (dY == nullptr || X == nullptr || g == nullptr || u == nullptr || WgT == nullptr ||
-      WuT == nullptr || WdT == nullptr)
+      WuT == nullptr || WdT == nullptr || (dX == nullptr && dWgT == nullptr && dWdT == nullptr))
     return SIG_ERR_NULL;
   const int bad = first_error({check_rows(dY, lddy, d_model), check_rows(X, ldx, d_model),
                                check_rows(dX, lddx, d_model)});

@@ -109,6 +109,17 @@ def test_gated_mlp_backward_validation(lib):
     assert backward(lib, ws=None) == WORKSPACE and backward(lib, ws_bytes=need - 1) == WORKSPACE
 
 
+def test_gated_mlp_backward_of_an_empty_block(lib):
+    """No tokens: whatever gradient is wanted, no pointer is looked at.  The gradient in
+    X of an empty tensor is a NULL pointer, so it cannot count as one that is missing."""
+    none = dict(rows=0, dY=None, X=None, g=None, u=None, dWgT=None, dWuT=None, dWdT=None, ws=None, ws_bytes=0)
+    assert backward(lib, dX=None, **none) == OK
+    assert backward(lib, **none) == OK
+    # one of the two projections' gradients alone stays an error, and so do bad sizes
+    assert backward(lib, **{**none, "dWgT": P}) == NULL and backward(lib, **{**none, "dWuT": P}) == NULL
+    assert backward(lib, **{**none, "d_model": 20}) == SHAPE and backward(lib, **{**none, "act": 5}) == ARG
+
+
 def test_workspace_sizes(lib):
     ws = lib.sig_workspace_bytes
     assert ws(10, 64, 8, 3) == 256 and ws(11, 64, 8, 3) == 3 * 256      # whole 256-byte parts

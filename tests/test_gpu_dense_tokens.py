@@ -468,6 +468,18 @@ def test_empty_blocks(sig):
     assert dX.shape == (0, 64) and all(bool((w == 0).all()) for w in dW)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_empty_block_with_a_part_of_the_gradients(sig, dtype):
+    """No tokens reached the block (frozen weights, or weight gradients alone)."""
+    X, W = normal(50, 0, 64, dtype=dtype), normal(51, 64, 32, dtype=dtype)
+    e, Wd = normal(52, 0, 32, dtype=dtype), W.T.contiguous()
+    dX, *none = sig.gated_mlp_backward(X, X, e, e, W, W, Wd, want_weights=False)
+    assert dX.shape == (0, 64) and none == [None] * 3
+    none, *dW = sig.gated_mlp_backward(X, X, e, e, W, W, Wd, want_x=False)
+    assert none is None and all(bool((w == 0).all()) for w in dW)
+    assert [w.shape for w in dW] == [(64, 32), (64, 32), (32, 64)]
+
+
 def test_refusals_of_the_binding(sig):
     import torch
     X, W = normal(52, 4, 64), normal(53, 64, 32)
