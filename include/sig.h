@@ -637,13 +637,16 @@ SIG_API int sig_take_device_error(unsigned* code, sig_stream_t stream);
 /*
  * Set the limit, in SM clock cycles, after which a pipeline wait of the
  * tensor-core GEMMs (nm_act_gemm, nm_act_gemm_ex, nm_act_gemm_packed,
- * linear_act, gated_mlp, gated_mlp_backward) gives up, on the current device; cycles <= 0 restores the default (4e9, about 2 s
- * at 1.9 GHz).  No counterpart on the pages: it lets a caller (or a test)
- * shorten the failure-detection window.  A kernel that gives up records a bit
- * in the device error word (sig_take_device_error), lets the copies it has
- * issued land (waiting up to the default limit for each), frees its tensor
- * memory and returns; its output is not valid.  Synchronous with respect to
- * the host (cudaMemcpyToSymbol); do not call it during stream capture.
+ * linear_act, gated_mlp, gated_mlp_backward) gives up, on the current device;
+ * cycles <= 0 restores the default (4e9, about 2 s at 1.9 GHz).  No counterpart
+ * on the pages: it lets a caller (or a test) shorten the failure-detection
+ * window.  In the last three some waits span all products of a tile, so a limit
+ * below that time may make sound calls give up.  A kernel that gives up records
+ * a bit in the device error word (sig_take_device_error), lets the copies it has
+ * issued land (waiting up to the default limit for each), frees its tensor memory
+ * and returns; its output is not valid (what linear_act has not finished is left
+ * as it was).  Synchronous with respect to the
+ * host (cudaMemcpyToSymbol); do not call it during stream capture.
  * Errors: SIG_ERR_CUDA.
  */
 SIG_API int sig_set_wait_limit(long long cycles);

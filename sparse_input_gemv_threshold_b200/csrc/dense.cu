@@ -128,6 +128,20 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
   return true;
 }
 
+// The few-token kernel's wait for its sums, whose barrier completes once every issued
+// MMA has finished, also when another wait has given up: tensor memory is kept until
+// then.  It covers all stages of the part, so it lasts for the default limit at least
+// (a shorter one is for the waits of a single stage); past that it has given up too.
+__device__ __forceinline__ bool wait_sums(uint32_t bar, long long limit) {
+  long long waited = 0;
+  while (!wait_drain(bar, 0u))
+    if ((waited += kDenseTimeout) > limit - kDenseTimeout) {
+      atomicOr(&g_dense_error, 1u);
+      return false;
+    }
+  return true;
+}
+
 // Hands an accumulator back: the tensor-memory loads are done and fenced, and no
 // other memory is passed on, so the arrive needs no release (whose wait for the
 // warp's earlier stores made 59 us of the 44 that 22016 x 4096 outputs of depth 16
@@ -495,6 +509,10 @@ __device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
 
 __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
   asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ void st_cluster_u8(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u8 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ void sts_b32(uint32_t addr, uint32_t v) {
@@ -1365,6 +1383,7 @@ struct FewBars {
   unsigned long long full[kFewMaxStages];
   unsigned long long empty[kFewMaxStages];
   unsigned long long accum;
+  alignas(8) uint8_t gave_up[kFewCluster];   // each part's verdict, written by it in every CTA of the cluster
   uint32_t tmem_base;
   int abort_flag;
   int consumed;
@@ -1477,21 +1496,29 @@ dense_few_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__
   const int own = (valid + ranks - 1) / ranks;     // rank r joins tokens [r own, (r + 1) own)
   Join<EPI, BF> last(args, mat, n0, t0 + rank * own, min(own, valid - rank * own));
 
-  const bool acc_done = wait_drain(smem_u32(&sm.accum), 0u);
-  // one verdict for the CTA: the tensor-memory loads below need whole warps
+  // one warp polls, the others wait at the barrier; one verdict for the CTA, since the
+  // tensor-memory loads below need whole warps
+  const bool acc_done = warp != 1 || wait_sums(smem_u32(&sm.accum), limit);
   const bool ok = __syncthreads_and(acc_done && !*abort_flag) != 0;
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *(volatile uint32_t*)&sm.tmem_base;
   if (ranks > 1) {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (fs.join == 0) cluster_sync();   // the ring is free once every CTA's MMAs are done
+    // and one for the cluster: a part that gave up is missing from every sum
+    if (warp == 0 && lane < ranks)
+      st_cluster_u8(map_to_rank(smem_u32(&sm.gave_up[rank]), (uint32_t)lane), ok ? 0u : 1u);
   }
   if (ok) join_send(smem_u32(join), tmem, warp, lane, valid, own, rank);
-  if (ranks > 1)
+  bool whole = ok;
+  if (ranks > 1) {
     cluster_sync();
-  else
+    const unsigned long long parts = *reinterpret_cast<volatile unsigned long long*>(sm.gave_up);
+    whole = whole && parts << (8 * (kFewCluster - ranks)) == 0ull;
+  } else {
     __syncthreads();
-  if (ok) last.finish(smem_u32(join), own, ranks);
+  }
+  if (whole) last.finish(smem_u32(join), own, ranks);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
   if (tid == 0 && *abort_flag)
