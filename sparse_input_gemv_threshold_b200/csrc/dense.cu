@@ -120,7 +120,8 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, vola
   return true;
 }
 
-// Not cut short by a give-up: lets issued copies and MMAs finish.
+// Not cut short by a give-up: lets issued copies and MMAs finish, so its limit is the
+// default whatever the launch's is.
 __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
   const long long t0 = clock64();
   while (!try_cluster(bar, parity))
@@ -715,6 +716,7 @@ struct PairBars {
   uint32_t tmem_base;
   int abort_flag;
   int consumed;
+  int brought[2];   // 0, or of a CTA that gave up 1 + the stages that it brought, see end_pair
 };
 
 // Item t of the walk: a tile of 256 accumulator columns, or, from `whole` on,
@@ -780,6 +782,37 @@ __device__ __forceinline__ void stage_store(uint32_t block, int lane, const CUte
   }
 }
 
+// The end of a pair's walk, with the MMAs done and every warp of the CTA here.  After a
+// give-up of either CTA, the copies that both issued land before shared memory goes.  A
+// stage that only one of them brought never completes, so each says how far it came (a
+// leader that waited for such a stage held the GPU for the default limit, 2 s, a stage);
+// the copies of those stages were issued a wait's limit ago, and land in the last pause.
+template <typename Bars>
+__device__ __forceinline__ void end_pair(Bars& sm, int stages, uint32_t rank, int issued, uint32_t tmem, int warp,
+                                         int lane) {
+  if (warp == 8 && lane < 2 && *(volatile int*)&sm.abort_flag)
+    st_cluster(map_to_rank(smem_u32(&sm.brought[rank]), (uint32_t)lane), (uint32_t)issued + 1u);
+  __syncthreads();
+  cluster_sync();
+  if (warp == 8)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                 : "memory");
+  const int a = *(volatile int*)&sm.brought[0], b = *(volatile int*)&sm.brought[1];
+  if ((a | b) == 0) return;
+  if (warp == 8 && lane == 0) {
+    // who did not give up has brought every stage
+    const int both = min(a > 0 ? a - 1 : 0x7fffffff, b > 0 ? b - 1 : 0x7fffffff);
+    if (rank == 0)
+      for (int it = sm.consumed; it < both; ++it)
+        wait_drain(smem_u32(&sm.full[it % stages]), (uint32_t)(it / stages) & 1u);
+    const long long t0 = clock64();
+    while (clock64() - t0 < 40000) {
+    }
+  }
+  __syncthreads();
+  cluster_sync();
+}
+
 template <bool A_MN, bool B_K, int EPI, bool BF>
 __global__ void __launch_bounds__(kPairThreads, 1)
 dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__ DenseArgs args) {
@@ -815,6 +848,7 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
     for (int w = 0; w < 16; ++w) mbar_init(smem_u32(&sm.extra[w / 2][w % 2]), 1);
     sm.abort_flag = 0;
     sm.consumed = 0;
+    sm.brought[0] = sm.brought[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -1000,7 +1034,7 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
             for (int j = 0; j < 4; ++j)
               sts16(wide_at(to, lane, part * 4 + j), pack8<BF>(*reinterpret_cast<float(*)[8]>(&v[8 * j])));
           }
-          stage_store(to, lane, &maps.o[p.mat], col, row0, p);
+          if (go) stage_store(to, lane, &maps.o[p.mat], col, row0, p);
         }
       } else if constexpr (EPI == DENSE_GATED) {
         // accumulator columns [0, bn / 2) are g, the others u; 64 hidden columns a
@@ -1068,7 +1102,7 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
           if (lane == 0) {
-            if (row0 < p.rows && col < p.cols)
+            if (go && row0 < p.rows && col < p.cols)
               for (int out = 0; out < 3; ++out) tma_store_2d(&maps.o[out], to + out * 2048u, col, row0);
             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
           }
@@ -1086,23 +1120,10 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
   }
 
   __syncthreads();
-  wait_drain(smem_u32(&sm.done), 0u);
+  if (__builtin_expect(!wait_drain(smem_u32(&sm.done), 0u), 0) && tid == 0) atomicOr(&g_dense_error, 1u);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == 8 && lane == 0 && *abort_flag) {
-    // after a give-up: the copies that were issued land before shared memory goes
-    if (leader)
-      for (int it = sm.consumed; it < issued; ++it)
-        wait_drain(smem_u32(&sm.full[it % S]), (uint32_t)(it / S) & 1u);
-    const long long t0 = clock64();
-    while (clock64() - t0 < 40000) {
-    }
-  }
-  __syncthreads();
-  cluster_sync();
-  if (warp == 8)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
-                 : "memory");
+  end_pair(sm, S, rank, issued, tmem, warp, lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -1130,6 +1151,7 @@ struct TallBars {
   uint32_t tmem_base;
   int abort_flag;
   int consumed;
+  int brought[2];   // 0, or of a CTA that gave up 1 + the stages that it brought, see end_pair
 };
 
 // Item t of the walk: token tile m, column tile n.  The token tiles of a group run
@@ -1187,6 +1209,7 @@ dense_tall_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
     mbar_init(smem_u32(&sm.done), 1);
     sm.abort_flag = 0;
     sm.consumed = 0;
+    sm.brought[0] = sm.brought[1] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
@@ -1350,23 +1373,10 @@ dense_tall_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
   }
 
   __syncthreads();
-  wait_drain(smem_u32(&sm.done), 0u);
+  if (__builtin_expect(!wait_drain(smem_u32(&sm.done), 0u), 0) && tid == 0) atomicOr(&g_dense_error, 1u);
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (warp == 8 && lane == 0 && *abort_flag) {
-    // after a give-up: the copies that were issued land before shared memory goes
-    if (leader)
-      for (int it = sm.consumed; it < issued; ++it)
-        wait_drain(smem_u32(&sm.full[it % S]), (uint32_t)(it / S) & 1u);
-    const long long start = clock64();
-    while (clock64() - start < 40000) {
-    }
-  }
-  __syncthreads();
-  cluster_sync();
-  if (warp == 8)
-    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
-                 : "memory");
+  end_pair(sm, S, rank, issued, tmem, warp, lane);
 }
 
 // ---------------------------------------------------------------------------

@@ -23,11 +23,13 @@ def under_limit(sig, limit, run):
         sig.set_wait_limit(0)
 
 
-# the few-token kernel with a join of several parts beside the ring and in its place.
+# the few-token kernel with a join of several parts beside the ring and in its place,
+# the tall kernel and the pair kernel, each with a residual that its epilogue reads.
 # The limits go from before the first load's arrival to past the whole product, so that
 # the CTAs of a cluster come to different verdicts in some of the calls.
 @pytest.mark.parametrize("rows,K,N", [
-    (5, 4096, 1000), (16, 11008, 4096), (48, 4096, 1000), (200, 4096, 520), (333, 4096, 1000)])
+    (5, 4096, 1000), (16, 11008, 4096), (48, 4096, 1000), (200, 4096, 520), (333, 4096, 1000),
+    (1300, 1000, 8200), (1281, 320, 5000)])
 def test_no_sum_with_a_missing_part_is_stored(sig, rows, K, N):
     import torch
     X, W, R = normal(1, rows, K), normal(2, K, N, scale=K ** -0.5), normal(3, rows, N)
@@ -56,3 +58,17 @@ def test_a_sum_of_many_stages_outlasts_a_stages_limit(sig):
     for limit in (30000, 20_000_000, 1 << 33):
         Y, code = under_limit(sig, limit, lambda: sig.linear_act(X, W))
         assert code == 0 and torch.equal(Y, want), limit
+
+
+@pytest.mark.parametrize("rows,K,N", [(1300, 1000, 8200), (1281, 320, 5000)])
+def test_a_pair_that_gives_up_waits_for_no_copy_that_was_not_issued(sig, rows, K, N):
+    """When one CTA of a pair stops a stage before the other, the stage's barrier never
+    completes; a wait for it would last for the default limit, 2 s."""
+    import time
+    X, W, R = normal(6, rows, K), normal(7, K, N, scale=K ** -0.5), normal(8, rows, N)
+    want = sig.linear_act(X, W, residual=R)
+    for limit in (600, 1500, 3000, 5000):
+        t0 = time.perf_counter()
+        _, code = under_limit(sig, limit, lambda: sig.linear_act(X, W, residual=R))
+        assert code != 0 and time.perf_counter() - t0 < 0.5, limit
+    assert bool((sig.linear_act(X, W, residual=R) == want).all())
