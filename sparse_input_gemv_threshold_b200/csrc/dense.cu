@@ -59,7 +59,7 @@ struct DenseArgs {
   int rows2, cols2, tm2, tn2;   // pair kernel: the second product of the launch (weight 2), if any
   int whole, items;    // pair kernel: tiles taken whole, and all items of the walk
   int group;           // tall kernel: token tiles walked together
-  int mats;
+  int mats;            // pair kernel: weights side by side
   int outs;            // outputs to store (DENSE_GATED: 1, or 3 with g and u)
   int act;
   bool plain;          // DENSE_LINEAR: no bias, activation or residual
@@ -144,9 +144,9 @@ __device__ __forceinline__ bool wait_sums(uint32_t bar, long long limit) {
 }
 
 // Hands an accumulator back: the tensor-memory loads are done and fenced, and no
-// other memory is passed on, so the arrive needs no release (whose wait for the
-// warp's earlier stores made 59 us of the 44 that 22016 x 4096 outputs of depth 16
-// take otherwise).
+// other memory is passed on, so the arrive needs no release, which waits for the
+// warp's earlier stores (22016 x 4096 outputs of depth 16: 59.4 us with one, 39.1
+// without).
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
@@ -579,12 +579,12 @@ struct Join {
   static constexpr int kLanes = EPI == DENSE_GATED ? 16 : 32;   // lanes of a token
   static constexpr int kStep = 256 / kLanes;                    // tokens that the CTA takes at once
   const DenseArgs& args;
-  int mat, row0, col, mine, slot, ch;
+  int row0, col, mine, slot, ch;
   float4 bias;
   Extra e[kJoin];
 
-  __device__ __forceinline__ Join(const DenseArgs& a, int m, int n0, int first, int tokens)
-      : args(a), mat(m), row0(first), mine(tokens), bias(make_float4(0.f, 0.f, 0.f, 0.f)) {
+  __device__ __forceinline__ Join(const DenseArgs& a, int n0, int first, int tokens)
+      : args(a), row0(first), mine(tokens), bias(make_float4(0.f, 0.f, 0.f, 0.f)) {
     slot = (int)threadIdx.x / kLanes;
     ch = (int)threadIdx.x % kLanes * 4;
     col = n0 + ch;
@@ -639,7 +639,7 @@ struct Join {
         for (int t = 0; t < kJoin; ++t)
           finish4<EPI, BF, decltype(A)::value>(v[t], w[t], bias, e[t], o[0][t], o[1][t], o[2][t]);
         const int64_t at = (int64_t)(row0 + s) * args.ldo + col, step = (int64_t)kStep * args.ldo;
-        store(args.o[EPI == DENSE_LINEAR ? mat : 0] + at, step, s, o[0]);
+        store(args.o[0] + at, step, s, o[0]);
         if (EPI == DENSE_GRAD || (EPI == DENSE_GATED && args.outs == 3)) {
           store(args.o[1] + at, step, s, o[1]);
           store(args.o[2] + at, step, s, o[2]);
@@ -659,18 +659,18 @@ struct Join {
 // The weight's boxes of K stage kb for a CTA's 128 accumulator lanes from
 // output column n0: each(map, coordinates, byte offset in the operand).
 template <bool B_K, int EPI, typename F>
-__device__ __forceinline__ void weight_boxes(const DenseMaps& maps, const DenseArgs& args, int mat, int n0,
-                                             int kb, F&& each) {
+__device__ __forceinline__ void weight_boxes(const DenseMaps& maps, const DenseArgs& args, int n0, int kb,
+                                             F&& each) {
   const int seg = kb >= args.kb0 ? 1 : 0;
   const int k = (kb - (seg ? args.kb0 : 0)) * kSlab;
   if constexpr (B_K) {
-    each(&maps.b[seg | mat], k, n0, 0u);
+    each(&maps.b[seg], k, n0, 0u);
   } else if constexpr (EPI == DENSE_GATED) {   // 64 columns of each weight: lanes 0 .. 63 g, 64 .. 127 u
     each(&maps.b[0], n0, k, 0u);
     each(&maps.b[1], n0, k, kBlock);
   } else {
-    each(&maps.b[seg | mat], n0, k, 0u);
-    each(&maps.b[seg | mat], n0 + 64, k, kBlock);
+    each(&maps.b[seg], n0, k, 0u);
+    each(&maps.b[seg], n0 + 64, k, kBlock);
   }
 }
 
@@ -1244,7 +1244,7 @@ dense_tall_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
         const uint32_t fb = full0 + (uint32_t)s * 8u, w0 = smem_u32(ring) + (uint32_t)s * stage_bytes;
         if (elect_one()) {
           if (leader) mbar_expect_tx(smem_u32(&sm.full[s]), 2 * stage_bytes);
-          weight_boxes<B_K, EPI>(maps, args, 0, n0, kb, [&](const CUtensorMap* map, int c0, int c1, uint32_t at) {
+          weight_boxes<B_K, EPI>(maps, args, n0, kb, [&](const CUtensorMap* map, int c0, int c1, uint32_t at) {
             tma_load_2d_pair(w0 + at, map, c0, c1, fb);
           });
           tma_load_2d_pair(w0 + kOperand, &maps.a[seg], (kb - (seg ? args.kb0 : 0)) * kSlab, t0, fb);
@@ -1419,9 +1419,8 @@ dense_few_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__
   uint8_t* join = fs.join > 0 ? ring + (size_t)S * stage_bytes : ring;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)blockIdx.x, ranks = (int)gridDim.x;   // the cluster spans the grid's x
-  const int mat = (int)blockIdx.y / args.tn, nt = (int)blockIdx.y - mat * args.tn;
   constexpr int kOutCols = EPI == DENSE_GATED ? 64 : 128;     // output columns of the tile
-  const int n0 = nt * kOutCols;
+  const int n0 = (int)blockIdx.y * kOutCols;
   const int t0 = (int)blockIdx.z * fs.tn;
   const int kb_lo = (int)((int64_t)args.kbt * rank / ranks);
   const int steps = (int)((int64_t)args.kbt * (rank + 1) / ranks) - kb_lo;
@@ -1457,7 +1456,7 @@ dense_few_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__
       const uint32_t fb = smem_u32(&sm.full[s]), w0 = smem_u32(ring) + (uint32_t)s * stage_bytes;
       if (elect_one()) {
         mbar_expect_tx(fb, stage_bytes);
-        weight_boxes<B_K, EPI>(maps, args, mat, n0, kb, [&](const CUtensorMap* map, int c0, int c1, uint32_t at) {
+        weight_boxes<B_K, EPI>(maps, args, n0, kb, [&](const CUtensorMap* map, int c0, int c1, uint32_t at) {
           tma_load_2d(w0 + at, map, c0, c1, fb);
         });
         tma_load_2d(w0 + kOperand, &maps.a[seg], k, t0, fb);
@@ -1504,7 +1503,7 @@ dense_few_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__
 
   const int valid = min(fs.tn, args.rows - t0);    // tokens of this tile
   const int own = (valid + ranks - 1) / ranks;     // rank r joins tokens [r own, (r + 1) own)
-  Join<EPI, BF> last(args, mat, n0, t0 + rank * own, min(own, valid - rank * own));
+  Join<EPI, BF> last(args, n0, t0 + rank * own, min(own, valid - rank * own));
 
   // one warp polls, the others wait at the barrier; one verdict for the CTA, since the
   // tensor-memory loads below need whole warps
@@ -1613,13 +1612,13 @@ DensePlan plan_dense(const DenseGemm& d, int kbt) {
   const DensePlan pair = {DENSE_PAIR, 0, 0, 0};
   if (d.a_mn) return pair;
   const int shrink = d.epi == DENSE_GATED ? 2 : 1;   // accumulator columns of an output column
-  const int cols = d.mats * ceil_div(d.cols * shrink, 128);
+  const int cols = ceil_div(d.cols * shrink, 128);
   if (d.rows <= 16) {
     int parts = std::min({kFewCluster, kbt, std::max({1, kbt / 32, 128 / cols})});
     while (parts > 1 && cols > kClusters2[parts]) --parts;
     return {DENSE_FEW, 16, parts, 2};
   }
-  const int tiles = ceil_div(d.rows, 256) * d.mats * ceil_div(d.cols * shrink, 256);
+  const int tiles = ceil_div(d.rows, 256) * ceil_div(d.cols * shrink, 256);
   const int waves = tiles / (kNumSMs / 2), left = tiles % (kNumSMs / 2);
   double best = 4.1 + kbt * (0.36 * waves + (left == 0 ? 0.0 : left <= kNumSMs / 4 ? 0.25 : 0.33));
   DensePlan plan = pair;
@@ -1731,7 +1730,7 @@ cudaError_t launch_few(const DensePlan& p, const DenseMaps& maps, const DenseArg
                         std::min(fit, ceil_div(args.kbt, p.parts))});
   const size_t smem = (size_t)fs.stages * stage_bytes + fs.join + extra;
   return launch_cluster<&dense_few_kernel<B_K, EPI, BF>>(
-      dim3((unsigned)p.parts, (unsigned)(args.tn * args.mats), (unsigned)args.tm), kFewThreads, p.parts, smem,
+      dim3((unsigned)p.parts, (unsigned)args.tn, (unsigned)args.tm), kFewThreads, p.parts, smem,
       stream, maps, args, fs);
 }
 
@@ -1770,6 +1769,7 @@ cudaError_t launch_typed(const DenseGemm& d, const DensePlan& p, const DenseMaps
 }  // namespace
 
 cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream) {
+  if (!d.a_mn && (d.mats != 1 || d.also != nullptr)) return cudaErrorInvalidValue;   // one weight, one product
   const int kb = ceil_div(d.K, kSlab), kbt = d.two_segments ? 2 * kb : kb;
   const DensePlan p = plan_dense(d, kbt);
   const bool dual = d.epi == DENSE_GATED;

@@ -14,8 +14,8 @@ enum DenseEpilogue : int {
   DENSE_GRAD = 2      // acc = dh, g and u given: dg = dh u act'(g), du = dh act(g), h = act(g) u
 };
 
-// One product of `rows` x `cols` outputs over K (two K segments when a1 is
-// given; two column blocks of `cols` when `mats` is 2).
+// One product of `rows` x `cols` outputs over K (two K segments with
+// `two_segments`; with a_mn, two column blocks of `cols` when `mats` is 2).
 struct DenseGemm {
   int epi = DENSE_LINEAR;
   bool bf16 = false;
@@ -29,7 +29,7 @@ struct DenseGemm {
   const uint16_t* b[2] = {};
   int64_t ldb = 0;
   bool two_segments = false;   // acc = A0 B0 + A1 B1, both of depth K
-  int mats = 1;                // 2: o[0] = A B0 and o[1] = A B1
+  int mats = 1;                // 2 (with a_mn only): o[0] = A B0 and o[1] = A B1
   int act = 0;
   const uint16_t* bias = nullptr;
   const uint16_t* residual = nullptr;
