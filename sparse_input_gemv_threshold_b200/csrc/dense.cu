@@ -1505,9 +1505,10 @@ dense_few_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant__
   const int own = (valid + ranks - 1) / ranks;     // rank r joins tokens [r own, (r + 1) own)
   Join<EPI, BF> last(args, n0, t0 + rank * own, min(own, valid - rank * own));
 
-  // one warp polls, the others wait at the barrier; one verdict for the CTA, since the
-  // tensor-memory loads below need whole warps
-  const bool acc_done = warp != 1 || wait_sums(smem_u32(&sm.accum), limit);
+  // Every warp polls: with one of them, and the others at the barrier, 333 x 4096 ->
+  // 4096 takes 16.9 us instead of 16.5.  One verdict for the CTA, since the
+  // tensor-memory loads below need whole warps.
+  const bool acc_done = wait_sums(smem_u32(&sm.accum), limit);
   const bool ok = __syncthreads_and(acc_done && !*abort_flag) != 0;
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = *(volatile uint32_t*)&sm.tmem_base;
