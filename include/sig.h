@@ -103,6 +103,17 @@ typedef enum {
   SIG_ACT_SILU = 4        /* z / (1 + exp(-z))                               */
 } sig_act;
 
+/* The products of linear_act, gated_mlp and gated_mlp_backward (sig_dense_plan). */
+typedef enum {
+  SIG_PRODUCT_LINEAR = 0,       /* X WT (d_in = K, d_out = N); the down projection too */
+  SIG_PRODUCT_GATED = 1,        /* X WgT and X WuT; from here on d_in = d_model, d_out = d_ff */
+  SIG_PRODUCT_HIDDEN_GRAD = 2,  /* dY WdT^T                                        */
+  SIG_PRODUCT_INPUT_GRAD = 3,   /* dg WgT^T + du WuT^T                             */
+  SIG_PRODUCT_UP_GRADS = 4,     /* X^T dg and X^T du, where dWdT is not wanted     */
+  SIG_PRODUCT_DOWN_GRAD = 5,    /* h^T dY, where dWgT and dWuT are not wanted      */
+  SIG_PRODUCT_WEIGHT_GRADS = 6  /* all three, in one launch                        */
+} sig_product;
+
 /* Largest activation length the fused mask prologue accepts. */
 #define SIG_MAX_D_IN 131072
 /* Largest length sparsify_topk accepts (its keys live in shared memory). */
@@ -623,6 +634,20 @@ SIG_API int gated_mlp_backward(const uint16_t* dY, int64_t lddy, const uint16_t*
                                int64_t d_model, int64_t d_ff, int act, uint16_t* dX, int64_t lddx,
                                uint16_t* dWgT, uint16_t* dWuT, uint16_t* dWdT, int dtype, void* ws,
                                size_t ws_bytes, sig_stream_t stream);
+
+/*
+ * How a product of the three calls above is run, for tests and for choosing block
+ * sizes (nothing is launched; the answer depends on the arguments alone):
+ *   plan[0]  the kernel: 0 CTA pairs with 256 x 256 tiles, 1 CTA pairs with the
+ *            tokens as the narrow operand, 2 one-CTA tiles for few tokens
+ *   plan[1]  tokens (rows of the output, for a weight gradient) of a tile
+ *   plan[2]  CTAs that share a tile's K       plan[3]  CTAs on an SM
+ *   plan[4]  tiles taken whole                plan[5]  half tiles
+ *   product  a sig_product, which says what d_in and d_out are.
+ * 1 <= rows <= 2^24, widths as in the call.
+ * Errors: SIG_ERR_NULL, SIG_ERR_ARG (product), SIG_ERR_SHAPE.
+ */
+SIG_API int sig_dense_plan(int product, int64_t rows, int64_t d_in, int64_t d_out, int* plan);
 
 /*
  * Read and clear the library's device error words (no counterpart on the

@@ -15,6 +15,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -29,7 +30,9 @@ __all__ = [
     "nm_packed_bytes", "sparsify_nm_packed", "nm_act_gemm_packed", "sparse_gemv_f8",
     "OP_SPARSE_GEMV_F8", "set_wait_limit", "sparse_gemv_q4", "OP_SPARSE_GEMV_Q4",
     "linear_act", "gated_mlp", "gated_mlp_backward", "ACT_NONE", "ACT_RELU", "ACT_GELU",
-    "ACT_GELU_TANH", "ACT_SILU", "OP_GATED_TOKENS", "OP_GATED_BACKWARD",
+    "ACT_GELU_TANH", "ACT_SILU", "OP_GATED_TOKENS", "OP_GATED_BACKWARD", "dense_plan", "DensePlan",
+    "PRODUCT_LINEAR", "PRODUCT_GATED", "PRODUCT_HIDDEN_GRAD", "PRODUCT_INPUT_GRAD",
+    "PRODUCT_UP_GRADS", "PRODUCT_DOWN_GRAD", "PRODUCT_WEIGHT_GRADS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsig.so")
@@ -42,6 +45,8 @@ OP_SPARSE_GEMV_Q4 = 9
 OP_GATED_TOKENS = 10
 OP_GATED_BACKWARD = 11
 ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = range(5)
+(PRODUCT_LINEAR, PRODUCT_GATED, PRODUCT_HIDDEN_GRAD, PRODUCT_INPUT_GRAD, PRODUCT_UP_GRADS,
+ PRODUCT_DOWN_GRAD, PRODUCT_WEIGHT_GRADS) = range(7)
 MAX_BATCH = 16
 MAX_D_IN = 131072
 
@@ -80,6 +85,7 @@ _SIGNATURES = {
                          _p, _i32, _p, _sz, _p]),
     "gated_mlp_backward": (_i32, [_p, _i64, _p, _i64, _i64, _p, _p, _p, _p, _p, _i64, _i64, _i32,
                                   _p, _i64, _p, _p, _p, _i32, _p, _sz, _p]),
+    "sig_dense_plan": (_i32, [_i32, _i64, _i64, _i64, ctypes.POINTER(_i32)]),
     "sig_col_sums": (_i32, [_p, _i64, _i64, _p, _p]),
     "teal_mlp_sparse": (_i32, [_p, _p, _p, _p, _i64, _i64, _f32, _f32, _p, _p, _p, _p, _sz, _p]),
 }
@@ -700,6 +706,25 @@ def gated_mlp_backward(dY, X, g, u, WgT, WuT, WdT, act: int = ACT_SILU, dX=None,
         WuT.data_ptr(), WdT.data_ptr(), m, f, act, _ptr(dX), lddx, _ptr(dWgT), _ptr(dWuT),
         _ptr(dWdT), dt, ws.data_ptr(), n, _raw_stream(X.get_device())))
     return dX, dWgT, dWuT, dWdT
+
+
+class DensePlan(NamedTuple):
+    """How a dense product is run (dense_plan)."""
+    kernel: str    # "pair", "tall" or "few"
+    tokens: int    # of a tile
+    parts: int     # CTAs that share a tile's K
+    per_sm: int    # CTAs on an SM
+    tiles: int     # taken whole
+    halves: int    # half tiles
+
+
+def dense_plan(product: int, rows: int, d_in: int, d_out: int) -> DensePlan:
+    """The kernel and the tiles that linear_act, gated_mlp or gated_mlp_backward uses for
+    one of its products (PRODUCT_...) over `rows` tokens.  d_in and d_out are K and N of
+    a linear product, d_model and d_ff of the others.  Nothing is launched."""
+    plan = (_i32 * 6)()
+    _check("sig_dense_plan", _lib.sig_dense_plan(product, rows, d_in, d_out, plan))
+    return DensePlan(("pair", "tall", "few")[plan[0]], *plan[1:])
 
 
 def take_device_error(stream=None) -> int:

@@ -55,6 +55,42 @@ int check_rows(const void* p, int64_t ld, int64_t width) {
   return ld % 8 == 0 && aligned16(p) ? SIG_OK : SIG_ERR_ALIGN;
 }
 
+// The products of the calls below, but for their pointers, strides and epilogue
+// arguments.  d_in and d_out are K and N of a linear product, d_model and d_ff of the
+// gated MLP's.
+DenseGemm dense_product(int product, int64_t rows, int64_t d_in, int64_t d_out) {
+  DenseGemm d;
+  switch (product) {
+    case SIG_PRODUCT_LINEAR:        // X WT
+      d.rows = rows; d.cols = d_out; d.K = d_in;
+      break;
+    case SIG_PRODUCT_GATED:         // X WgT and X WuT
+      d.epi = DENSE_GATED;
+      d.rows = rows; d.cols = d_out; d.K = d_in;
+      break;
+    case SIG_PRODUCT_HIDDEN_GRAD:   // dY WdT^T
+      d.epi = DENSE_GRAD;
+      d.rows = rows; d.cols = d_out; d.K = d_in;
+      d.b_k = true;
+      break;
+    case SIG_PRODUCT_INPUT_GRAD:    // dg WgT^T + du WuT^T, one sum over both
+      d.rows = rows; d.cols = d_in; d.K = d_out;
+      d.b_k = true;
+      d.two_segments = true;
+      break;
+    case SIG_PRODUCT_UP_GRADS:      // X^T dg and X^T du
+      d.rows = d_in; d.cols = d_out; d.K = rows;
+      d.a_mn = true;
+      d.mats = 2;
+      break;
+    case SIG_PRODUCT_DOWN_GRAD:     // h^T dY
+      d.rows = d_out; d.cols = d_in; d.K = rows;
+      d.a_mn = true;
+      break;
+  }
+  return d;
+}
+
 int first_error(std::initializer_list<int> checks) {
   for (int c : checks)
     if (c != SIG_OK) return c;
@@ -487,9 +523,8 @@ int linear_act(const uint16_t* X, int64_t rows, int64_t K, int64_t ldx, const ui
   if (!aligned16(WT) || !aligned16(bias)) return SIG_ERR_ALIGN;
   // other tiles still read X while Y is written; a residual in Y's place has Y's rows
   if (Y == X || (Y == residual && ldy != ldr)) return SIG_ERR_ARG;
-  DenseGemm d;
+  DenseGemm d = dense_product(SIG_PRODUCT_LINEAR, rows, K, N);
   d.bf16 = dtype == SIG_BF16;
-  d.rows = rows; d.cols = N; d.K = K;
   d.a[0] = X; d.lda = ldx;
   d.b[0] = WT; d.ldb = N;
   d.act = act; d.bias = bias; d.residual = residual; d.ldr = ldr;
@@ -522,19 +557,16 @@ int gated_mlp(const uint16_t* X, int64_t rows, int64_t ldx, const uint16_t* WgT,
   }
   uint16_t* h = h_out != nullptr ? h_out : static_cast<uint16_t*>(ws);
 
-  DenseGemm up;
-  up.epi = DENSE_GATED;
+  DenseGemm up = dense_product(SIG_PRODUCT_GATED, rows, d_model, d_ff);
   up.bf16 = dtype == SIG_BF16;
-  up.rows = rows; up.cols = d_ff; up.K = d_model;
   up.a[0] = X; up.lda = ldx;
   up.b[0] = WgT; up.b[1] = WuT; up.ldb = d_ff;
   up.act = act;
   up.o[0] = h; up.o[1] = g_out; up.o[2] = u_out; up.ldo = d_ff;
   if (launch_dense(up, (cudaStream_t)stream) != cudaSuccess) return SIG_ERR_CUDA;
 
-  DenseGemm dn;
+  DenseGemm dn = dense_product(SIG_PRODUCT_LINEAR, rows, d_ff, d_model);
   dn.bf16 = up.bf16;
-  dn.rows = rows; dn.cols = d_model; dn.K = d_ff;
   dn.a[0] = h; dn.lda = d_ff;
   dn.b[0] = WdT; dn.ldb = d_model;
   dn.residual = residual; dn.ldr = ldr;
@@ -578,36 +610,33 @@ int gated_mlp_backward(const uint16_t* dY, int64_t lddy, const uint16_t* X, int6
   uint16_t* h = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + 2 * hb);
   const bool bf16 = dtype == SIG_BF16;
 
-  DenseGemm dh;   // dh = dY WdT^T; dg, du and h from it, g and u
-  dh.epi = DENSE_GRAD;
+  // dh = dY WdT^T; dg, du and h from it, g and u
+  DenseGemm dh = dense_product(SIG_PRODUCT_HIDDEN_GRAD, rows, d_model, d_ff);
   dh.bf16 = bf16;
-  dh.rows = rows; dh.cols = d_ff; dh.K = d_model;
   dh.a[0] = dY; dh.lda = lddy;
-  dh.b_k = true; dh.b[0] = WdT; dh.ldb = d_model;
+  dh.b[0] = WdT; dh.ldb = d_model;
   dh.act = act; dh.g = g; dh.u = u;
   dh.o[0] = dg; dh.o[1] = du; dh.o[2] = h; dh.ldo = d_ff;
   if (launch_dense(dh, st) != cudaSuccess) return SIG_ERR_CUDA;
 
-  if (dX != nullptr) {   // dX = dg WgT^T + du WuT^T, one sum over both
-    DenseGemm x;
+  if (dX != nullptr) {   // dX = dg WgT^T + du WuT^T
+    DenseGemm x = dense_product(SIG_PRODUCT_INPUT_GRAD, rows, d_model, d_ff);
     x.bf16 = bf16;
-    x.rows = rows; x.cols = d_model; x.K = d_ff;
-    x.two_segments = true;
     x.a[0] = dg; x.a[1] = du; x.lda = d_ff;
-    x.b_k = true; x.b[0] = WgT; x.b[1] = WuT; x.ldb = d_ff;
+    x.b[0] = WgT; x.b[1] = WuT; x.ldb = d_ff;
     x.o[0] = dX; x.ldo = lddx;
     if (launch_dense(x, st) != cudaSuccess) return SIG_ERR_CUDA;
   }
-  DenseGemm up;   // dWgT = X^T dg and dWuT = X^T du
+  // dWgT = X^T dg and dWuT = X^T du
+  DenseGemm up = dense_product(SIG_PRODUCT_UP_GRADS, rows, d_model, d_ff);
   up.bf16 = bf16;
-  up.rows = d_model; up.cols = d_ff; up.K = rows;
-  up.a_mn = true; up.a[0] = X; up.lda = ldx;
-  up.mats = 2; up.b[0] = dg; up.b[1] = du; up.ldb = d_ff;
+  up.a[0] = X; up.lda = ldx;
+  up.b[0] = dg; up.b[1] = du; up.ldb = d_ff;
   up.o[0] = dWgT; up.o[1] = dWuT; up.ldo = d_ff;
-  DenseGemm down;   // dWdT = h^T dY
+  // dWdT = h^T dY
+  DenseGemm down = dense_product(SIG_PRODUCT_DOWN_GRAD, rows, d_model, d_ff);
   down.bf16 = bf16;
-  down.rows = d_ff; down.cols = d_model; down.K = rows;
-  down.a_mn = true; down.a[0] = h; down.lda = d_ff;
+  down.a[0] = h; down.lda = d_ff;
   down.b[0] = dY; down.ldb = lddy;
   down.o[0] = dWdT; down.ldo = d_model;
   if (dWgT != nullptr) {   // one launch for all that is wanted
@@ -615,6 +644,22 @@ int gated_mlp_backward(const uint16_t* dY, int64_t lddy, const uint16_t* X, int6
     return cuda_status(launch_dense(up, st));
   }
   return dWdT != nullptr ? cuda_status(launch_dense(down, st)) : SIG_OK;
+}
+
+int sig_dense_plan(int product, int64_t rows, int64_t d_in, int64_t d_out, int* plan) {
+  if (plan == nullptr) return SIG_ERR_NULL;
+  if (product < SIG_PRODUCT_LINEAR || product > SIG_PRODUCT_WEIGHT_GRADS) return SIG_ERR_ARG;
+  const bool in_ok = product == SIG_PRODUCT_LINEAR ? d_in >= 1 && d_in <= kMaxWidth : dense_width(d_in);
+  if (rows < 1 || rows > kMaxRows || !in_ok || !dense_width(d_out)) return SIG_ERR_SHAPE;
+  const bool both = product == SIG_PRODUCT_WEIGHT_GRADS;
+  DenseGemm d = dense_product(both ? SIG_PRODUCT_UP_GRADS : product, rows, d_in, d_out);
+  const DenseGemm down = dense_product(SIG_PRODUCT_DOWN_GRAD, rows, d_in, d_out);
+  if (both) d.also = &down;
+  const DensePlan p = plan_dense(d);
+  const DenseTiles t = tile_dense(d, p);
+  const int out[6] = {p.kind, p.tn, p.parts, p.per_sm, t.whole, t.items - t.whole};
+  std::copy(out, out + 6, plan);
+  return SIG_OK;
 }
 
 int sig_set_wait_limit(long long cycles) {

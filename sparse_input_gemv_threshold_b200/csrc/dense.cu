@@ -1560,17 +1560,11 @@ bool map16(CUtensorMap* map, const void* base, int64_t inner, int64_t outer, int
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// How a product is run: by the pair kernel, by the tall kernel with tiles of tn
-// tokens, or by the few-token kernel with tiles of tn tokens, `parts` CTAs along K
-// and per_sm CTAs resident on an SM.
-enum DenseKind { DENSE_PAIR, DENSE_TALL, DENSE_FEW };
-
-struct DensePlan {
-  DenseKind kind;
-  int tn, parts, per_sm;
-};
-
 int ceil_div(int64_t a, int64_t b) { return (int)((a + b - 1) / b); }
+
+// K stages of a product, and of one of its segments
+int segment_stages(const DenseGemm& d) { return ceil_div(d.K, kSlab); }
+int all_stages(const DenseGemm& d) { return segment_stages(d) * (d.two_segments ? 2 : 1); }
 
 // Clusters of 1 .. 8 CTAs are placed within a GPC, so fewer of the larger ones
 // fit at once: what cudaOccupancyMaxActiveClusters gives for the few-token
@@ -1609,8 +1603,11 @@ constexpr int kClusters2[kFewCluster + 1] = {0, 296, 148, 93, 71, 56, 45, 37, 33
 // 11.1, tall 12.1.
 constexpr int kGroupTiles = 16;   // token tiles the tall kernel walks together (4096 x 4096 -> 11008 in
                                   // tiles of 208: 276 us, 281 with 4; 16384 x 4096 -> 4096: 405, 413 with all)
-DensePlan plan_dense(const DenseGemm& d, int kbt) {
-  const DensePlan pair = {DENSE_PAIR, 0, 0, 0};
+}  // namespace
+
+DensePlan plan_dense(const DenseGemm& d) {
+  const int kbt = all_stages(d);
+  const DensePlan pair = {DENSE_PAIR, 256, 1, 1};
   if (d.a_mn) return pair;
   const int shrink = d.epi == DENSE_GATED ? 2 : 1;   // accumulator columns of an output column
   const int cols = ceil_div(d.cols * shrink, 128);
@@ -1657,6 +1654,26 @@ DensePlan plan_dense(const DenseGemm& d, int kbt) {
   }
   return plan;
 }
+
+DenseTiles tile_dense(const DenseGemm& d, const DensePlan& p) {
+  DenseTiles t = {};
+  t.tm = ceil_div(d.rows, p.tn);
+  t.tn = ceil_div(d.cols, (p.kind == DENSE_FEW ? 128 : 256) / (d.epi == DENSE_GATED ? 2 : 1));
+  t.whole = t.items = t.tm * t.tn;
+  if (p.kind == DENSE_PAIR) {
+    if (d.also != nullptr) {
+      t.tm2 = ceil_div(d.also->rows, 256);
+      t.tn2 = ceil_div(d.also->cols, 256);
+    }
+    const int tiles = t.tm * t.tn * d.mats + t.tm2 * t.tn2, left = tiles % (kNumSMs / 2);
+    const bool cut = left <= kNumSMs / 4;   // a remainder of at most half a wave is cut in two
+    t.whole = cut ? tiles - left : tiles;
+    t.items = cut ? tiles + left : tiles;
+  }
+  return t;
+}
+
+namespace {
 
 // `FN` may use all the shared memory of a CTA: asked for once per device.
 template <auto FN>
@@ -1771,32 +1788,27 @@ cudaError_t launch_typed(const DenseGemm& d, const DensePlan& p, const DenseMaps
 
 cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream) {
   if (!d.a_mn && (d.mats != 1 || d.also != nullptr)) return cudaErrorInvalidValue;   // one weight, one product
-  const int kb = ceil_div(d.K, kSlab), kbt = d.two_segments ? 2 * kb : kb;
-  const DensePlan p = plan_dense(d, kbt);
+  const DensePlan p = plan_dense(d);
+  const DenseTiles t = tile_dense(d, p);
   const bool dual = d.epi == DENSE_GATED;
   DenseMaps maps = {};
   DenseArgs a = {};
   a.rows = (int)d.rows;
   a.cols = (int)d.cols;
-  a.kb0 = kb;
-  a.kbt = kbt;
+  a.kb0 = segment_stages(d);
+  a.kbt = all_stages(d);
   const bool pair = p.kind == DENSE_PAIR;
-  a.tm = ceil_div(d.rows, pair ? 256 : p.tn);
-  a.tn = ceil_div(d.cols, (p.kind == DENSE_FEW ? 128 : 256) / (dual ? 2 : 1));
+  a.tm = t.tm;
+  a.tn = t.tn;
+  a.tm2 = t.tm2;
+  a.tn2 = t.tn2;
+  a.whole = t.whole;
+  a.items = t.items;
   a.mats = d.mats;
-  a.items = a.tm * a.tn;
   a.group = kGroupTiles;
-  if (pair) {
-    if (d.also != nullptr) {
-      a.rows2 = (int)d.also->rows;
-      a.cols2 = (int)d.also->cols;
-      a.tm2 = ceil_div(a.rows2, 256);
-      a.tn2 = ceil_div(a.cols2, 256);
-    }
-    const int tiles = a.tm * a.tn * a.mats + a.tm2 * a.tn2, left = tiles % (kNumSMs / 2);
-    const bool cut = left <= kNumSMs / 4;   // a remainder of at most half a wave is cut in two
-    a.whole = cut ? tiles - left : tiles;
-    a.items = cut ? tiles + left : tiles;
+  if (d.also != nullptr) {
+    a.rows2 = (int)d.also->rows;
+    a.cols2 = (int)d.also->cols;
   }
   a.outs = dual ? (d.o[1] != nullptr ? 3 : 1) : 1;
   a.act = d.act;

@@ -42,6 +42,26 @@ struct DenseGemm {
   const DenseGemm* also = nullptr;
 };
 
+// How a product is run: by the pair kernel, by the tall kernel with tiles of tn
+// tokens, or by the few-token kernel with tiles of tn tokens, `parts` CTAs along K
+// and per_sm CTAs resident on an SM.
+enum DenseKind { DENSE_PAIR = 0, DENSE_TALL = 1, DENSE_FEW = 2 };
+
+struct DensePlan {
+  DenseKind kind;
+  int tn, parts, per_sm;
+};
+
+// Its tiles: tm down and tn across one weight (pair kernel: tm2 and tn2 of the second
+// product of the launch too), of which the first `whole` are taken whole and the
+// others in two halves (pair kernel only); `items` steps of the walk in all.
+struct DenseTiles {
+  int tm, tn, tm2, tn2, whole, items;
+};
+
+DensePlan plan_dense(const DenseGemm& d);
+DenseTiles tile_dense(const DenseGemm& d, const DensePlan& p);
+
 cudaError_t launch_dense(const DenseGemm& d, cudaStream_t stream);
 cudaError_t read_dense_error(unsigned* out, cudaStream_t stream);
 cudaError_t set_dense_wait_limit(long long cycles);
