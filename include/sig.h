@@ -94,7 +94,11 @@ typedef enum {
   SIG_BF16 = 1   /* bfloat16: the upper half of an IEEE binary32       */
 } sig_dtype;
 
-/* Activations of linear_act, gated_mlp and gated_mlp_backward, in float32. */
+/* Activations of linear_act, gated_mlp and gated_mlp_backward, act(z) = z p(z), in
+ * float32.  The share p has a relative error of at most about (16 + z^2) 2^-23 (GELU),
+ * (4 + 1.3 |z|) 2^-23 (SiLU) and (4 + 3.3 y) 2^-23 with y = 2 sqrt(2/pi) |z + 0.044715
+ * z^3| (tanh form) in the lower tail; a share under 2^-126 (z below -13.1, -87 and -10)
+ * is 0, and so is the slope there.  -inf gives NaN (its share is 0) but for ReLU, 0. */
 typedef enum {
   SIG_ACT_NONE = 0,       /* z                                               */
   SIG_ACT_RELU = 1,       /* max(z, 0); slope 0 at z = 0, NaN stays NaN      */

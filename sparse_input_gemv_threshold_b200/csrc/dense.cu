@@ -292,9 +292,13 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack2<BF>(f[6], f[7]));
 }
 
-constexpr float kInvSqrt2 = 0.70710678118654752f;
-constexpr float kErfP = 0.3275911f;   // Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26
-constexpr float kErfA[5] = {0.254829592f, -0.284496736f, 1.421413741f, -1.453152027f, 1.061405429f};
+// Phi(-x) exp(x^2 / 2) = t P(t), t = 1 / (1 + p x): P of degree 7, fitted by weighted
+// least squares (Lawson's iteration) to the smallest largest relative error over
+// 0 <= x <= 14, 1.1e-7 with these float32 coefficients.
+constexpr float kTailP = 0.304f;
+constexpr float kTailA[8] = {0.121236868f, 0.122136548f, 0.102640741f, 0.122816235f,
+                             -0.0417008735f, 0.19059512f, -0.154348761f, 0.036624115f};
+constexpr float kHalfLog2E = 0.72134752044448170f;   // log2(e) / 2
 constexpr float kInvSqrt2Pi = 0.39894228040143268f;
 constexpr float kGeluC = 0.79788456080286536f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
@@ -304,16 +308,32 @@ constexpr float kGeluA = 0.044715f;
 // the IEEE division 2048 x 1024 -> 2816 took 25.0 us with SiLU, now 15.1).
 __device__ __forceinline__ float logistic(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 
-// exp(-z^2 / 2)
-__device__ __forceinline__ float bell(float z) { return __expf(-0.5f * z * z); }
+// 1 / v for v >= 1, and exp(-z^2 / 2) as a power of two: the hardware's instructions
+// without the steps for subnormal values, which the first has none of and the second
+// gives as 0 (beyond |z| = 13.2).
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ float bell(float z) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(z * (-kHalfLog2E * z)));
+  return r;
+}
 
-// The normal distribution function, from Abramowitz and Stegun's erfc(x) =
-// t (a1 + t (a2 + ..)) exp(-x^2), t = 1 / (1 + p x), good to 1.5e-7 for x >= 0.
-// Its exponential is the one that the slope of GELU needs too.
+// The normal distribution function.  Its lower tail has a small relative error, about
+// (16 + z^2) 2^-23, which an error that is small against one (such as the five
+// coefficients of Abramowitz and Stegun's 7.1.26, used before: 1.5e-7) is not: that is
+// past half a step of bf16 below z = -6.2.  Its three more multiply-adds cost less than
+// the two plain instructions save: 2048 x 1024 -> 2816 with GELU and residual 17.7 us,
+// 18.9 with __fdividef and __expf, 18.5 with the five coefficients and these.  The
+// exponential is the one that the slope of GELU needs too.
 __device__ __forceinline__ float normal_cdf(float z) {
-  const float t = __fdividef(1.f, fmaf(kErfP * kInvSqrt2, fabsf(z), 1.f));
-  const float poly = fmaf(t, fmaf(t, fmaf(t, fmaf(t, kErfA[4], kErfA[3]), kErfA[2]), kErfA[1]), kErfA[0]);
-  const float tail = 0.5f * t * poly * bell(z);
+  const float t = reciprocal(fmaf(kTailP, fabsf(z), 1.f));
+  const float high = fmaf(t, fmaf(t, fmaf(t, kTailA[7], kTailA[6]), kTailA[5]), kTailA[4]);
+  const float poly = fmaf(t, fmaf(t, fmaf(t, fmaf(t, high, kTailA[3]), kTailA[2]), kTailA[1]), kTailA[0]);
+  const float tail = t * poly * bell(z);
   return z >= 0.f ? 1.f - tail : tail;
 }
 
