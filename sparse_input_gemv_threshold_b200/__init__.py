@@ -528,7 +528,8 @@ def nm_act_gemm(X, WT, n: int, m: int, Y=None, ws=None, stream=None):
 # Dense products for blocks of tokens.  Their calls run on the tensors' own
 # device, on `stream` or that device's current stream; what they allocate
 # (outputs, and a workspace per call) belongs to that stream, so calls on
-# different streams and captured graphs share nothing.
+# different streams and captured graphs share nothing.  Like every function
+# here they are outside autograd.
 
 _DTYPES = {torch.float16: 0, torch.bfloat16: 1}
 
@@ -597,7 +598,8 @@ def linear_act(X, WT, bias=None, act: int = ACT_NONE, residual=None, Y=None, str
 
     X (rows, K), WT (K, N) contiguous, bias (N,), residual and Y (rows, N);
     X, residual and Y may have row strides (multiples of 8).  Y may be the
-    residual.  N must be a multiple of 8."""
+    residual.  N must be a multiple of 8.  Y carries no gradient, whatever the inputs
+    require: autograd does not see the call."""
     dt, rows, K = _block(X, "X")
     ctx = _elsewhere(X, stream)
     if ctx is not None:
@@ -631,7 +633,8 @@ def gated_mlp(X, WgT, WuT, WdT, act: int = ACT_SILU, residual=None, Y=None, h_ou
     X, residual and Y (rows, d_model), row strides allowed; WgT, WuT
     (d_model, d_ff) and WdT (d_ff, d_model) contiguous.  h_out, g_out and u_out
     (rows, d_ff) receive the hidden block and the two projections, which
-    gated_mlp_backward takes."""
+    gated_mlp_backward takes.  Y carries no gradient, whatever the inputs require:
+    autograd does not see the call, and gated_mlp_backward is called by name."""
     dt, rows, m = _block(X, "X")
     ctx = _elsewhere(X, stream)
     if ctx is not None:
@@ -668,7 +671,8 @@ def gated_mlp_backward(dY, X, g, u, WgT, WuT, WdT, act: int = ACT_SILU, dX=None,
     output and the g and u that it kept.
 
     want_x or want_weights False leaves those out (None in their place).  Given
-    gradient tensors are written, not added to."""
+    gradient tensors are written, not added to; no .grad is touched.  The gradient of
+    gated_mlp's residual is dY itself."""
     dt, rows, m = _block(X, "X")
     ctx = _elsewhere(X, stream)
     if ctx is not None:

@@ -841,3 +841,14 @@ def test_a_wait_that_gives_up_is_reported(sig, rows):
     assert torch.equal(sig.linear_act(X, W), want)
     assert sig.take_device_error() == 0
     assert np.isfinite(want.float().cpu().numpy()).all()
+
+
+def test_calls_are_outside_autograd(sig):
+    """As documented: outputs carry no gradient, and no .grad is touched."""
+    import torch
+    args = [t.requires_grad_() for t in backward_inputs(5, 64, 136, "bf16", seed=300)]
+    Y = sig.gated_mlp(args[1], *args[4:])
+    outs = [Y, sig.linear_act(args[1], args[4]), *sig.gated_mlp_backward(*args)]
+    assert not any(t.requires_grad for t in outs) and all(t.grad is None for t in args)
+    with torch.no_grad():
+        assert torch.equal(Y, sig.gated_mlp(args[1], *args[4:]))
