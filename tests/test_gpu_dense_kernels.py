@@ -187,3 +187,48 @@ def test_a_wait_that_gives_up_is_reported_by_every_kernel(sig):
         _, code = under_limit(sig, 64, lambda: sig.linear_act(X, W))
         assert code == 1, kernel
         assert torch.equal(sig.linear_act(X, W), want) and sig.take_device_error() == 0
+
+
+# ---------------------------------------------------------------------------
+# The limits of the sizes
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("rows,K,N", [(1, 1 << 20, 8), (300, 1 << 20, 8), (3, 8, 1 << 20), (1300, 8, 1 << 20),
+                                      (1 << 24, 8, 8), ((1 << 24) - 5, 72, 8)])
+def test_largest_sizes(sig, rows, K, N):
+    import torch
+    X, W = normal(310, rows, K), normal(311, K, N, scale=K ** -0.5)
+    b = normal(312, N)
+    Y = sig.linear_act(X, W, bias=b, act=sig.ACT_RELU)
+    at = torch.unique(torch.cat([torch.randint(0, rows, (300,), generator=torch.Generator().manual_seed(3)),
+                                 torch.tensor([0, rows - 1])])).cuda()
+    z, e = tokens.product(X[at], W)
+    z = z + b.double()
+    y, e = z.clamp(min=0.0), e + tokens.U * z.abs()
+    tokens.within(Y[at], y, tokens.rounding(y, e, "fp16"), f"{rows}x{K}x{N}")
+
+
+def test_largest_sizes_of_the_gated_block(sig):
+    """2^24 tokens forward, and weight gradients that sum over 2^20 + 3 of them."""
+    import torch
+    rows = 1 << 24
+    X, Wg, Wu, Wd = normal(320, rows, 8), normal(321, 8, 8), normal(322, 8, 8), normal(323, 8, 8)
+    Y = sig.gated_mlp(X, Wg, Wu, Wd, residual=X)
+    for at in (slice(0, 300), slice(rows - 300, rows), slice(1 << 23, (1 << 23) + 300)):
+        assert torch.equal(Y[at], sig.gated_mlp(X[at].contiguous(), Wg, Wu, Wd, residual=X[at].contiguous()))
+    rows = (1 << 20) + 3
+    tokens.test_gated_mlp_backward(sig, "fp16", rows, 8, 16, "silu")
+
+
+def test_largest_stride(sig):
+    """Two rows 2^30 entries apart: X, the residual and Y, whose gap stays as it was."""
+    import torch
+    ld, K, N = 1 << 30, 72, 136
+    buf = [torch.empty(ld + N, dtype=torch.float16, device="cuda") for _ in range(2)]
+    X, R = (b.as_strided((2, c), (ld, 1)) for b, c in zip(buf, (K, N)))
+    X.copy_(normal(330, 2, K))
+    R.copy_(normal(331, 2, N))
+    buf[1][N:ld] = 7.0
+    W = normal(332, K, N, scale=0.1)
+    want = sig.linear_act(X.contiguous(), W, residual=R.contiguous())
+    sig.linear_act(X, W, residual=R, Y=R)
+    assert torch.equal(R, want) and bool((buf[1][N:ld] == 7).all())
