@@ -5,15 +5,16 @@
 //   dense_pair_kernel  persistent: CTA pairs walk tiles of 256 tokens x 256 (or
 //                      128) columns with two accumulators in tensor memory, so
 //                      the epilogue of a tile runs beside the mainloop of the
-//                      next.  Bound by the tensor cores at the power limit:
-//                      4096 x 4096 x 4096 fp16 in 91-94 us on B200 (1.5 PFLOP/s,
-//                      0.9 of the measured burst rate; 77 % of the launch with
-//                      the tensor pipe active at 1.55 GHz).  Weight gradients, and
-//                      the shapes that its tiles fit better than the tall kernel's.
+//                      next.  Bound by the tensor cores at the power limit: the
+//                      weight gradients of 2048 tokens 4096/11008 bf16 in 357-375
+//                      us on B200 (1.5 PFLOP/s, 0.9 of the measured burst rate; 85 %
+//                      of the launch with the tensor pipe active at 1.52 GHz).  All
+//                      weight gradients, and the shapes that its tiles fit better
+//                      than the tall kernel's (shallow ones of many tokens).
 //   dense_tall_kernel  persistent, with the weight as the MMA's M operand and the
 //                      tokens as N: tiles of 256 columns x any multiple of 16
 //                      tokens, the height chosen so that the tiles fill whole
-//                      waves.  1300 x 4096 -> 11008 fp16 86 us (1.36 PFLOP/s; the
+//                      waves.  1300 x 4096 -> 11008 fp16 85 us (1.38 PFLOP/s; the
 //                      tensor pipe active in 88 % of the SMs' active cycles).
 //   dense_few_kernel   few tokens, bound by reading the weight: the weight is the
 //                      MMA's M operand (128 of its columns, one a tensor-memory
@@ -21,9 +22,9 @@
 //                      whose CTAs each take a part of K and join their float32
 //                      sums through distributed shared memory in a fixed order:
 //                      no workspace, no atomics, the same bits in every run.
-//                      16 tokens 4096 -> 11008: 17.4 us, 5.2 TB/s of weight
-//                      (0.79 of the measured copy rate); 1 token 4096 -> 4096
-//                      8.4 us, of which 5.1 are the weight at that rate.
+//                      16 tokens 4096 -> 11008: 18.4 us, 4.9 TB/s of weight
+//                      (0.75 of the measured copy rate); 1 token 4096 -> 4096
+//                      8.7 us, of which 5.1 are the weight at that rate.
 #include "common.cuh"
 #include "dense.h"
 #include "internal.h"
@@ -1157,8 +1158,8 @@ dense_pair_kernel(const __grid_constant__ DenseMaps maps, const __grid_constant_
 // column of 16 tokens at a time; four warps turn them over in shared memory, from
 // which each takes four tokens, 4 columns a lane.  Bound by the tensor cores (88 %
 // of the SMs' active cycles at 1300 x 4096 -> 11008), below about 150 tokens a tile
-// by a stage's bytes: 333 x 4096 -> 11008 in tiles of 112 33 us, 777 in tiles of 208
-// 56 us.
+// by a stage's bytes: 333 x 4096 -> 11008 in tiles of 112 35 us, 777 in tiles of 160
+// 55 us.
 // ---------------------------------------------------------------------------
 constexpr uint32_t kTurn = 16 * 128 * 4;   // 16 tokens x 128 columns of float32; four warps have two
 constexpr int kTallMaxStages = 8;
@@ -1587,8 +1588,9 @@ int segment_stages(const DenseGemm& d) { return ceil_div(d.K, kSlab); }
 int all_stages(const DenseGemm& d) { return segment_stages(d) * (d.two_segments ? 2 : 1); }
 
 // Clusters of 1 .. 8 CTAs are placed within a GPC, so fewer of the larger ones
-// fit at once: what cudaOccupancyMaxActiveClusters gives for the few-token
-// kernel's shared memory with one and with two CTAs on an SM.
+// fit at once: what cudaOccupancyMaxActiveClusters gave on a B200 for the few-token
+// kernel's shared memory with one and with two CTAs on an SM.  Where another card's
+// GPCs differ, the choice below is off, never a result.
 constexpr int kClusters1[kFewCluster + 1] = {0, 148, 74, 45, 33, 26, 22, 15, 15};
 constexpr int kClusters2[kFewCluster + 1] = {0, 296, 148, 93, 71, 56, 45, 37, 33};
 
