@@ -132,12 +132,13 @@ __device__ __forceinline__ bool wait_drain(uint32_t bar, uint32_t parity) {
 
 // The few-token kernel's wait for its sums, whose barrier completes once every issued
 // MMA has finished, also when another wait has given up: tensor memory is kept until
-// then.  It covers all stages of the part, so it lasts for the default limit at least
-// (a shorter one is for the waits of a single stage); past that it has given up too.
+// then.  It covers all stages of the part, so a limit for the waits of a single stage is
+// too short for it: it lasts for the launch's limit rounded up to whole default limits,
+// and has given up after that too.
 __device__ __forceinline__ bool wait_sums(uint32_t bar, long long limit) {
   long long waited = 0;
   while (!wait_drain(bar, 0u))
-    if ((waited += kDenseTimeout) > limit - kDenseTimeout) {
+    if ((waited += kDenseTimeout) >= limit) {
       atomicOr(&g_dense_error, 1u);
       return false;
     }
